@@ -302,6 +302,7 @@ muonh_status muonh_momentum_norm_noalloc(float* m, const float* g, int64_t rows,
 
 #define MUONH_DTYPE_F32 0
 #define MUONH_DTYPE_BF16 1
+#define MUONH_DTYPE_F16 2            /* layer norm, block-scaled products, orthogonalize */
 #define MUONH_AVERAGE_MAX_INPUTS 16
 #define MUONH_ADAMW_MAX_TENSORS 32   /* per launch; longer lists take several */
 
@@ -350,6 +351,46 @@ typedef struct {
  * ceil(n / MUONH_ADAMW_MAX_TENSORS) launches.  Tensors must not overlap. */
 muonh_status muonh_adamw_step(const muonh_adamw_tensor* tensors, int32_t n, const muonh_adamw_config* cfg,
                               int64_t step, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the update: the layers whose gradients the optimizers
+ * read.  Stateless; enqueued on `stream`; scratch is the caller's.
+ * ------------------------------------------------------------------------- */
+
+/* Layer norm of `rows` rows of n elements, and the RMS norm of a
+ * Qwen3-architecture model (its norm weights are in the AdamW group, Puro-2B
+ * report Table 8):
+ *   mu = <x>,  rstd = 1/sqrt(<(x - mu)^2> + eps),  y = (x - mu) rstd w + b
+ * with < > the mean over a row.  mean == NULL asks for the RMS norm (mu = 0).
+ *   x, y     device rows of dtype (MUONH_DTYPE_*), row strides ldx, ldy >= n
+ *            elements; y may be x.  Rows that start on 16-byte boundaries and
+ *            hold whole 16-byte vectors move by vectors, others by elements.
+ *   weight   n fp32 factors, or NULL for ones; bias n fp32, or NULL for none.
+ *   mean, rstd   `rows` fp32 results, for the backward pass; rstd != NULL.
+ * Sums are fp32.  A row that holds NaN or Inf gives NaN.  rows == 0 enqueues
+ * nothing (the buffers may be NULL). */
+muonh_status muonh_layer_norm(const void* x, int64_t ldx, void* y, int64_t ldy, const float* weight,
+                              const float* bias, float* mean, float* rstd, int64_t rows, int64_t n, int32_t dtype,
+                              float eps, void* stream);
+
+/* Bytes of scratch that muonh_layer_norm_backward needs for the weight sums. */
+size_t muonh_layer_norm_workspace(int64_t rows, int64_t n);
+
+/* Its gradients, with xh = (x - mu) rstd and g = dy w:
+ *   dx = rstd (g - <g> - xh <g xh>)      (no <g> term where mean == NULL)
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   mean, rstd  as the forward call wrote them; weight as it was given.
+ *   dx          of dtype; must not overlap x, and not dy unless n <= 8192.
+ *   dweight, dbias  n fp32 each, overwritten (what muonh_adamw_step reads as
+ *               g); NULL where not wanted.  rows == 0 writes zeros.
+ *   workspace   device scratch of at least muonh_layer_norm_workspace bytes,
+ *               4-byte aligned; may be NULL where dweight and dbias are.
+ * The sums over the rows are fp32 in a fixed order: the same bits for the same
+ * inputs on the same kind of device. */
+muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                       const float* weight, const float* mean, const float* rstd, void* dx,
+                                       int64_t lddx, float* dweight, float* dbias, int64_t rows, int64_t n,
+                                       int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Diagnostic of the failure path every pipelined kernel uses (the report has
  * no counterpart).  Launches one thread that waits on an mbarrier nothing

@@ -26,9 +26,10 @@ EXPORTED_SYMBOLS = (
     "muonh_export_state", "muonh_import_state", "muonh_device_status", "muonh_last_launch_count",
     "muonh_enable_timing", "muonh_phase_times", "muonh_phase_flops", "muonh_momentum_norm_noalloc",
     "muonh_average",
-    "muonh_adamw_step", "muonh_check_wait_timeout", "muonh_destroy", "muonh_status_string", "muonh_last_error",
+    "muonh_adamw_step", "muonh_layer_norm", "muonh_layer_norm_workspace", "muonh_layer_norm_backward",
+    "muonh_check_wait_timeout", "muonh_destroy", "muonh_status_string", "muonh_last_error",
 )
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 AVERAGE_MAX_INPUTS = 16
 ADAMW_MAX_TENSORS = 32
 PHASES = ("momentum_norm", "finalize_input", "write_x", "ns_gram", "ns_square", "ns_apply",
@@ -101,6 +102,13 @@ def library() -> ctypes.CDLL:
                                                 c_int32, c_void_p, c_void_p]
     lib.muonh_average.argtypes = [c_void_p, c_int32, POINTER(c_void_p), c_int32, c_int32, c_int64, c_void_p]
     lib.muonh_adamw_step.argtypes = [POINTER(AdamWTensor), c_int32, POINTER(AdamWConfig), c_int64, c_void_p]
+    lib.muonh_layer_norm.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_int64, c_int64, c_int32, c_float, c_void_p]
+    lib.muonh_layer_norm_workspace.argtypes = [c_int64, c_int64]
+    lib.muonh_layer_norm_workspace.restype = c_size_t
+    lib.muonh_layer_norm_backward.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int32,
+                                              c_void_p, c_size_t, c_void_p]
     lib.muonh_check_wait_timeout.argtypes = [ctypes.c_double, c_void_p]
     lib.muonh_destroy.argtypes = [c_void_p]
     lib.muonh_destroy.restype = None
@@ -111,7 +119,8 @@ def library() -> ctypes.CDLL:
     for name in ("muonh_init", "muonh_step", "muonh_step_device", "muonh_get_stats", "muonh_get_update", "muonh_get_radius",
                  "muonh_export_state", "muonh_import_state", "muonh_device_status",
                  "muonh_enable_timing", "muonh_phase_times", "muonh_phase_flops", "muonh_momentum_norm_noalloc",
-                 "muonh_average", "muonh_adamw_step", "muonh_check_wait_timeout"):
+                 "muonh_average", "muonh_adamw_step", "muonh_check_wait_timeout", "muonh_layer_norm",
+                 "muonh_layer_norm_backward"):
         getattr(lib, name).restype = c_int32
     _LIB = lib
     return lib

@@ -1,0 +1,141 @@
+"""ctypes bindings of the operators around the update: layer norm.
+
+Like the rest of the binding these calls check and marshal arguments; the work
+is in the library's CUDA kernels.  Each call runs on the device of its tensors,
+on `stream` or that device's current stream.  A given stream is also the one
+that results and scratch are allocated on, as under `torch.cuda.stream(stream)`.
+"""
+from __future__ import annotations
+
+import contextlib
+
+from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, _check, library
+
+
+def _dtype_code(dtype):
+    import torch
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    return codes.get(dtype)
+
+
+def _tensor(t, what: str, dtypes, device=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{what} must be a CUDA tensor of dtype {', '.join(map(str, dtypes))}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} must be on {device}, like the other tensors")
+    return t
+
+
+@contextlib.contextmanager
+def _on_other(device, stream):
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _on(device, stream):
+    """Context in which a call's allocations and launches belong to `device` and
+    `stream`; gives the stream's handle."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext(torch.cuda.current_stream().cuda_stream)
+    return _on_other(device, stream)
+
+
+def _rows(t, what: str):
+    """(pointer, rows, n, row stride) of a tensor seen as rows of its last
+    dimension; ValueError where one stride does not lead from row to row."""
+    n = t.shape[-1]
+    rows = 1
+    for d in t.shape[:-1]:
+        rows *= d
+    if t.is_contiguous():
+        return t.data_ptr(), rows, n, n
+    if n > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+    ld, expect = None, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != expect:
+            raise ValueError(f"{what} must be rows one stride apart (call .contiguous())")
+        expect = stride * size
+    ld = n if ld is None else ld
+    if rows > 1 and ld < n:
+        raise ValueError(f"{what} must have rows that do not overlap")
+    return t.data_ptr(), rows, n, ld
+
+
+def _vector(t, what: str, n: int, device):
+    import torch
+    if t is None:
+        return None
+    _tensor(t, what, (torch.float32,), device)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=None):
+    """Layer norm over the last dimension of x (fp32, bf16 or fp16), or the RMS
+    norm with rms=True: y = (x - mean) rstd weight + bias.  weight and bias are
+    fp32, as adamw_step keeps them.  Returns (y, mean, rstd): y in x's type (or
+    `out`, which may be x), mean (None for the RMS norm) and rstd fp32, one per
+    row, for layer_norm_backward."""
+    import torch
+    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least one element")
+    xp, rows, n, ldx = _rows(x, "x")
+    wp = _vector(weight, "weight", n, x.device)
+    bp = _vector(bias, "bias", n, x.device)
+    with _on(x.device, stream) as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _tensor(out, "out", (x.dtype,), x.device)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        op, _, _, ldo = _rows(out, "out")
+        mean = None if rms else torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _check(library().muonh_layer_norm(xp, ldx, op, ldo, wp, bp, None if rms else mean.data_ptr(),
+                                          rstd.data_ptr(), rows, n, _dtype_code(x.dtype), eps, handle))
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
+    """Gradients of layer_norm at x for the gradient dy of its result (x's shape
+    and type): (dx, dweight, dbias).  mean and rstd are what layer_norm gave;
+    mean None means the RMS norm.  dweight (None where weight is None) and dbias
+    (None unless bias is true) are fp32, as adamw_step reads them."""
+    import torch
+    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    _tensor(dy, "dy", (x.dtype,), x.device)
+    if x.dim() < 1 or x.shape[-1] < 1 or dy.shape != x.shape:
+        raise ValueError("dy and x must have the same shape, with a last dimension of at least one element")
+    xp, rows, n, ldx = _rows(x, "x")
+    dyp, _, _, lddy = _rows(dy, "dy")
+    wp = _vector(weight, "weight", n, x.device)
+    mp = _vector(mean, "mean", rows, x.device)
+    rp = _vector(rstd, "rstd", rows, x.device)
+    if rp is None:
+        raise TypeError("rstd must be given")
+    lib = library()
+    with _on(x.device, stream) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dweight = None if weight is None else torch.empty(weight.shape, dtype=torch.float32, device=x.device)
+        dbias = torch.empty(n, dtype=torch.float32, device=x.device) if bias else None
+        size = lib.muonh_layer_norm_workspace(rows, n) if weight is not None or bias else 0
+        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+        _check(lib.muonh_layer_norm_backward(
+            dyp, lddy, xp, ldx, wp, mp, rp, dx.data_ptr(), n, None if dweight is None else dweight.data_ptr(),
+            None if dbias is None else dbias.data_ptr(), rows, n, _dtype_code(x.dtype),
+            None if work is None else work.data_ptr(), size, handle))
+    return dx, dweight, dbias
