@@ -39,7 +39,8 @@
  *     on the calling thread is in muonh_last_error().
  *   - Conditions found on the device (non-finite input, zero update, a
  *     bounded wait that gave up) never abort a step: they set per-matrix
- *     flags in muonh_stats and are reported by muonh_device_status().
+ *     flags in muonh_stats and are reported by muonh_device_status() (of an
+ *     operator without a context: by muonh_operator_status()).
  *   - A context is not thread-safe: calls on one context must not overlap
  *     in time.  Distinct contexts are independent.  The context-free
  *     functions (averaging, AdamW, the diagnostics) are reentrant, except
@@ -391,6 +392,45 @@ muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void*
                                        const float* weight, const float* mean, const float* rstd, void* dx,
                                        int64_t lddx, float* dweight, float* dbias, int64_t rows, int64_t n,
                                        int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Orthogonalise a stack of matrices with a small side, for example one update
+ * per attention head (the step's own Newton-Schulz run takes whole matrices).
+ * For each of `batch` matrices X (rows x cols, min(rows, cols) <= 128), on its
+ * wide orientation:
+ *   Y = X/(||X||_F + eps);  ns_steps times: A = Y Y^T, Y <- (a I + b A + c A A) Y
+ *   x, out      16-bit device matrices of dtype (MUONH_DTYPE_BF16 or _F16), row
+ *               strides ldx, ldo >= cols and matrix strides x_stride,
+ *               out_stride in elements.  out may be x with the same strides;
+ *               otherwise they must not overlap.
+ *   ns_steps    0 .. 16;  eps >= 0 (a matrix of zeros gives zeros).
+ * The result is off by the rounding to its type and, for an ill-conditioned X,
+ * up to about 1e-3 of ||out|| (the r x r iterates are kept to 22 bits).
+ * ||X||_F^2 is held in fp32, so norms must be below 1.8e19; a matrix that holds
+ * NaN or Inf gives NaN throughout and leaves the others alone.
+ *   workspace   16-byte aligned device scratch of muonh_orthogonalize_workspace
+ *               bytes: 0 where base pointers and strides are multiples of 16
+ *               bytes, else room for a copy of the stacks that are not.
+ * UNSUPPORTED where the smaller side is above 128. */
+typedef struct {
+  const void* x;
+  void* out;
+  int64_t batch, rows, cols;
+  int64_t x_stride, ldx;
+  int64_t out_stride, ldo;
+  int32_t dtype;
+  int32_t ns_steps;
+  float ns_a, ns_b, ns_c;
+  float eps;
+} muonh_orthogonalize_desc;
+
+size_t muonh_orthogonalize_workspace(const muonh_orthogonalize_desc* desc);
+muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* desc, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* MUONH_ERR_TIMEOUT if a device wait gave up in an operator call above since
+ * the previous call (then clears the record), else OK; synchronises `stream`,
+ * which must be the one, or ordered after the ones, that the calls ran on. */
+muonh_status muonh_operator_status(void* stream);
 
 /* Diagnostic of the failure path every pipelined kernel uses (the report has
  * no counterpart).  Launches one thread that waits on an mbarrier nothing

@@ -33,3 +33,19 @@ def layer_norm_backward(dy, x, weight, mean, rstd, rms=False):
     if not rms:
         dx = dx - g.sum(1, keepdims=True) / n
     return rstd * dx, (dy * xh).sum(0), dy.sum(0)
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(x, steps=5, coeffs=QUINTIC, eps=1e-7):
+    """The Newton-Schulz output of each matrix of the stack x [batch, rows, cols]."""
+    a, b, c = coeffs
+    x = np.asarray(x, dtype=np.float64)
+    tall = x.shape[1] > x.shape[2]
+    y = x.transpose(0, 2, 1) if tall else x
+    y = y / (np.sqrt((y * y).sum((1, 2), keepdims=True)) + eps)
+    for _ in range(steps):
+        gram = y @ y.transpose(0, 2, 1)
+        y = a * y + (b * gram + c * (gram @ gram)) @ y
+    return y.transpose(0, 2, 1) if tall else y

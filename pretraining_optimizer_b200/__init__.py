@@ -11,4 +11,6 @@ from .muonh import (  # noqa: F401
     FLAG_TIMEOUT, PHASES, library, library_path, EXPORTED_SYMBOLS, momentum_norm_noalloc,
     average, adamw_step, check_wait_timeout,
 )
-from .operators import layer_norm, layer_norm_backward  # noqa: F401
+from .operators import (  # noqa: F401
+    layer_norm, layer_norm_backward, operator_status, orthogonalize,
+)

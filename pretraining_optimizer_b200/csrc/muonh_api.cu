@@ -196,6 +196,55 @@ int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 void muonh::set_error_message(const char* msg) { g_last_error = msg; }
 
+void muonh::ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq) {
+  // the bounds sample the scalar maps at thousands of points; a program uses
+  // one set of coefficients over and over
+  struct Memo {
+    float a, b, c;
+    int steps = -1;
+    int32_t ea, eb;
+    std::vector<int32_t> eq;
+  };
+  static thread_local Memo memo;
+  if (memo.steps != steps || memo.a != a || memo.b != b || memo.c != c) {
+    int32_t ex, ec;
+    scale_exponents(a, b, c, steps, P_FP16, &ex, &memo.ea, &ec, &memo.eb);
+    const double smax = iterate_bound(a, b, c, steps);
+    memo.eq.clear();
+    for (int k = 0; k < steps; ++k) memo.eq.push_back(q_exponent(a, b, c, k + 1, smax));
+    memo.a = a;
+    memo.b = b;
+    memo.c = c;
+    memo.steps = steps;
+  }
+  *ea = memo.ea;
+  *eb = memo.eb;
+  std::copy(memo.eq.begin(), memo.eq.end(), eq);
+}
+
+bool muonh::encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t cols, int64_t rows, int64_t batch,
+                               int64_t ld, int64_t stride, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(stride * 2)};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+extern "C" muonh_status muonh_operator_status(void* stream) {
+  set_error_message("");
+  int gave_up = 0;
+  if (take_orth_timeout(&gave_up, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return fail(MUONH_ERR_CUDA, "reading the operators' status failed");
+  if (gave_up) return fail(MUONH_ERR_TIMEOUT, "a device-side bounded wait gave up");
+  return MUONH_OK;
+}
+
 struct muonh_ctx {
   int32_t n = 0;
   int32_t prec = 0;

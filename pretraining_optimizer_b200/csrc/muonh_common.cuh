@@ -439,6 +439,20 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int ab_bf16, int 
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Power-of-two scales of the fp16 operands of a Newton-Schulz run on r x r
+// matrices: of A (and A p(A)), of p(A), and of the product of the first k + 1
+// factors p(A_0) ... p(A_k) in eq[k].
+void ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq);
+
+// 3-D map over a stack of 16-bit matrices (`batch` of rows x cols, row stride
+// ld and matrix stride `stride` in elements) with 64-column boxes of
+// box_rows rows (128-byte swizzle).
+bool encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t cols, int64_t rows, int64_t batch,
+                        int64_t ld, int64_t stride, int box_rows);
+
+// Reads and clears the record that a bounded wait gave up; synchronises s.
+cudaError_t take_orth_timeout(int* flag, cudaStream_t s);
+
 // Message returned by muonh_last_error() on the calling thread.
 void set_error_message(const char* msg);
 

@@ -1,0 +1,687 @@
+// Orthogonalising stacks of matrices with a small side (at most 128): one
+// Newton-Schulz update per attention head (sm_100a).
+//
+// For each matrix X (r x c on its wide orientation, r <= 128)
+//   Y = s X,  s = 1/(||X||_F + eps);   n times: A = Y Y^T, Y <- p(A) Y,
+//   p(A) = a I + b A + c A^2
+// Every iterate is a polynomial in A_0 = Y Y^T times Y, so the whole iteration
+// runs on r x r matrices (they commute, and stay symmetric):
+//   P_k = p(A_k),  A_{k+1} = (A_k P_k) P_k,  Q_{k+1} = Q_k P_k,   O = s Q_n X.
+// X is read once for the Gram matrix X X^T, whose trace is ||X||_F^2 (so the
+// scale needs no pass of its own), and once more, out of L2, for Q X; O is
+// written once.  Nothing r x c is kept in between.
+//
+// One cluster of 1 to 8 CTAs computes one matrix; a CTA walks over its share
+// of the 128-wide slices of the long side.  A slice of X is 128 x 128 in
+// shared memory, loaded by TMA as two boxes of 64 columns (128-byte swizzle),
+// and serves every product without being moved:
+//             wide X (r x c)                     tall X (c x r)
+//   Gram      both operands K-major              both operands MN-major
+//   Q X, X Q  Q K-major, slice MN-major          slice K-major, Q MN-major
+// The clusters' Gram shares are added through distributed shared memory, in
+// rank order, and every CTA then runs the same r x r iteration: with few
+// matrices the SMs would otherwise be idle, with many the cluster is one CTA.
+//
+// Precision.  The products are 16-bit with fp32 accumulation.  X X^T is exact
+// up to the accumulation: X is used as it is.  The r x r operands are kept as
+// fp16 pairs (hi + lo, 22 bits) and each product is hi hi + hi lo + lo hi:
+// with single fp16 operands the Gram-space form loses the small singular
+// directions (errors of 0.1 and more on ill-conditioned updates, by emulation,
+// against 2e-4 with pairs).  Q enters the last product as a pair of X's type.
+// The tensor cores' accumulation truncates, so at most kGramChunk slices are
+// accumulated in TMEM before they are added in IEEE fp32 registers.
+// The result is rounded once to X's type.
+#include <algorithm>
+#include <cmath>
+
+#include "muonh_common.cuh"
+
+namespace muonh {
+namespace {
+
+constexpr int kSide = 128;                        // padded small side; also the slice width
+constexpr int kChunkBytes = kSide * 64 * 2;       // 128 rows x 64 columns, 16-bit: 16 KB
+constexpr int kSliceBytes = 2 * kChunkBytes;      // one slice of X, or one r x r 16-bit matrix
+constexpr int kPairBytes = 2 * kSliceBytes;       // an r x r operand as hi and lo
+constexpr int kRing = 4;                          // slices in flight
+constexpr int kQOffset = kRing * kSliceBytes;     // the ring's space doubles as the operands A and P
+constexpr int kBarsOffset = kQOffset + kPairBytes;
+constexpr int kOrthSmem = kBarsOffset + 1024 + 1024;   // barriers, scalars; alignment slack
+static_assert(kRing * kSliceBytes == 2 * kPairBytes, "A and P share the ring's space");
+static_assert(kOrthSmem <= 227 * 1024, "shared memory of the orthogonalize kernel exceeds 227 KB");
+constexpr int kEpiThreads = 256;                  // 8 epilogue warps
+constexpr int kOrthThreads = 64 + kEpiThreads;    // warp 0 TMA, warp 1 MMA
+constexpr int kGramChunk = 16;                    // slices (2048 columns) per TMEM accumulation
+constexpr int kMaxSteps = 16;
+constexpr int kMaxCluster = 8;
+
+__device__ int g_orth_timeout;                    // a wait gave up in some call since the flag was read
+
+struct OrthParams {
+  int32_t slices;            // 128-wide slices of the long side
+  int32_t tall;              // X is c x r
+  int32_t steps;
+  float a, b, c, eps;
+  // power-of-two scales of the stored fp16 operands: A and A P; P; Q after
+  // step k; and the final Q
+  int32_t ea, eb, eq[kMaxSteps], eq_last;
+  int32_t rows, cols;        // of X, for skipping stores outside
+};
+
+__device__ __forceinline__ uint32_t row_piece(int row, int piece) {
+  return static_cast<uint32_t>(row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
+  if (!BF16) return pack_f16(lo, hi);
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack_16(uint32_t u) {
+  if (!BF16) return __half22float2(*reinterpret_cast<__half2*>(&u));
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u));
+}
+
+// 32 values of one row as a 16-bit pair hi + lo: pieces piece0 .. piece0 + 3
+// of the row in the 64-column chunk at `hi`, and the same in the lo matrix.
+template <bool BF16>
+__device__ __forceinline__ void store_split(uint8_t* hi, int row, int piece0, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[8 * q + 2 * i], y = v[8 * q + 2 * i + 1];
+      h[i] = pack_16<BF16>(x, y);
+      const float2 back = unpack_16<BF16>(h[i]);
+      l[i] = pack_16<BF16>(x - back.x, y - back.y);
+    }
+    const uint32_t at = row_piece(row, piece0 + q);
+    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(hi + kSliceBytes + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+}
+
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// D (+)= L R for the 128 x 128 pairs at l and r: L K-major, R MN-major, both
+// as their rows are stored.  R is symmetric up to rounding, but reading it as
+// its transpose (K-major) compounds that asymmetry from product to product: the
+// last A_k was off by 1e-4 instead of 1e-6.
+__device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r, uint32_t idesc) {
+  for (int prod = 0; prod < 3; ++prod) {          // hi hi, hi lo, lo hi
+    const uint32_t lo_l = l + (prod == 2 ? kSliceBytes : 0), lo_r = r + (prod == 1 ? kSliceBytes : 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      umma_f16(d, sdesc_sw128(lo_l + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
+               sdesc_sw128(lo_r + k * 2048, kChunkBytes, 1024), idesc, (prod | k) != 0);
+    }
+  }
+}
+
+// 16 bytes of another CTA's shared memory.
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <bool BF16>
+__global__ void __launch_bounds__(kOrthThreads, 1)
+    orthogonalize_kernel(const __grid_constant__ OrthParams p, const __grid_constant__ CUtensorMap xmap,
+                         const __grid_constant__ CUtensorMap omap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sm_a = smem;                     // A, then A P
+  uint8_t* const sm_p = smem + kPairBytes;
+  uint8_t* const sm_q = smem + kQOffset;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarsOffset);   // [pass][slot]
+  uint64_t* empty = full + 2 * kRing;             // [pass][slot]; pass 0: products done, pass 1: output stored
+  uint64_t* tfull = empty + 2 * kRing;            // [pass][accumulator]
+  uint64_t* tempty = tfull + 4;
+  uint64_t* ready = tempty + 4;                   // the epilogue wrote the next r x r operand
+  uint64_t* q_ready = ready + 1;                  // ... the final Q; the ring's space is free again
+  uint64_t* done = q_ready + 1;                   // a product of the A chain
+  uint64_t* done_q = done + 1;                    // a product of the Q chain
+  uint64_t* drain = done_q + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* err = reinterpret_cast<int*>(tmem_slot + 1);
+  float* trace = reinterpret_cast<float*>(err + 1);   // [8]: the epilogue warps' shares
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t ranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const uint32_t rank = cluster_ctarank();
+  const int matrix = blockIdx.x / ranks;
+  const int first = static_cast<int>(static_cast<int64_t>(p.slices) * rank / ranks);
+  const int count = static_cast<int>(static_cast<int64_t>(p.slices) * (rank + 1) / ranks) - first;
+  const int chunks = (count + kGramChunk - 1) / kGramChunk;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&full[kRing + s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&empty[kRing + s], kEpiThreads / 32);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], kEpiThreads);
+    }
+    mbar_init(ready, kEpiThreads);
+    mbar_init(q_ready, kEpiThreads);
+    mbar_init(done, 1);
+    mbar_init(done_q, 1);
+    mbar_init(drain, 1);
+    *err = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_d = tmem + 256, tm_q = tmem + 384;   // r x r products; slice products use columns 0 .. 255
+
+  // One walk of the producer over this CTA's slices.  A copy in flight lands
+  // before the CTA may exit: the MMA issuer or, after a wait that gave up,
+  // the producer itself waits for it.
+  auto produce = [&](int pass) {
+    uint64_t* f = full + pass * kRing;
+    uint64_t* e = empty + pass * kRing;
+    int i = 0;
+    for (; i < count; ++i) {
+      const int slot = i % kRing;
+      if (i >= kRing && !mbar_wait(&e[slot], (i / kRing - 1) & 1, err)) break;
+      mbar_expect_tx(&f[slot], kSliceBytes);
+      uint8_t* dst = smem + slot * kSliceBytes;
+      const int at = (first + i) * kSide;
+      for (int h = 0; h < 2; ++h)
+        tma_load_3d(dst + h * kChunkBytes, &xmap, &f[slot], p.tall ? 64 * h : at + 64 * h, p.tall ? at : 0, matrix);
+    }
+    for (int j = i > kRing ? i - kRing : 0; j < i; ++j) {
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&f[j % kRing], (j / kRing) & 1) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+  };
+
+  // epilogue threads: one row and 64 of its columns each (a warp reaches the
+  // TMEM lanes of its number mod 4)
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  const int row = quarter * 32 + lane, col0 = half * 64;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  const int ch = half * kChunkBytes;               // this thread's 64-column chunk
+  float acc[64];                                   // its part of X X^T, then of A_k
+
+  // ------------------------------------------------------------ X X^T
+  if (warp == 0) {
+    if (lane == 0) produce(0);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(kSide, kSide, BF16, p.tall) | (static_cast<uint32_t>(p.tall) << 15);
+      bool ok = true;
+      for (int i = 0; i < count && ok; ++i) {
+        const int slot = i % kRing, chunk = i / kGramChunk;
+        if (i % kGramChunk == 0 && chunk >= 2) ok = mbar_wait(&tempty[chunk & 1], ((chunk >> 1) - 1) & 1, err);
+        ok = ok && mbar_wait(&full[slot], (i / kRing) & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t d = p.tall ? sdesc_sw128(x + k * 2048, kChunkBytes, 1024)
+                                    : sdesc_sw128(x + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
+          umma_f16(tmem + (chunk & 1) * kSide, d, d, idesc, (i % kGramChunk) != 0 || k != 0);
+        }
+        umma_commit(&empty[slot]);
+        if (i % kGramChunk == kGramChunk - 1 || i == count - 1) umma_commit(&tfull[chunk & 1]);
+      }
+    }
+    __syncwarp();
+  } else {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+    for (int c = 0; c < chunks; ++c) {
+      if (!mbar_wait(&tfull[c & 1], (c >> 1) & 1, err)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float v[32];
+        tmem_ld32(tmem + lanes + (c & 1) * kSide + col0 + 32 * g, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[32 * g + j] += v[j];
+      }
+      tc_fence_before();
+      mbar_arrive(&tempty[c & 1]);
+    }
+    if (ranks > 1) {   // this CTA's share, for the others to add
+      float4* mine = reinterpret_cast<float4*>(smem) + (threadIdx.x - 64);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        mine[j * kEpiThreads] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+    }
+  }
+  if (ranks > 1) {
+    cluster_sync();
+    if (warp >= 2) {
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+      for (uint32_t r = 0; r < ranks; ++r) {
+        const uint32_t theirs = map_shared_rank(smem, r) + (threadIdx.x - 64) * 16;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float4 v = load_cluster(theirs + j * kEpiThreads * 16);
+          acc[4 * j] += v.x;
+          acc[4 * j + 1] += v.y;
+          acc[4 * j + 2] += v.z;
+          acc[4 * j + 3] += v.w;
+        }
+      }
+    }
+    cluster_sync();
+  }
+
+  // ------------------------------------------------- the r x r iteration
+  float scale = 0.f;                                // 1 / (||X|| + eps)
+  if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(kSide, kSide, 0, 1);
+      const uint32_t a = smem_u32(sm_a), pp = smem_u32(sm_p), q = smem_u32(sm_q);
+      int waits = 0;
+      auto wait_ready = [&] {
+        const bool ok = mbar_wait(ready, waits++ & 1, err);
+        tc_fence_after();
+        return ok;
+      };
+      for (int k = 0; k < p.steps; ++k) {
+        if (!wait_ready()) break;                   // A_k
+        pair_product(tm_d, a, a, idesc);
+        umma_commit(done);
+        if (!wait_ready()) break;                   // P_k
+        if (k < p.steps - 1) {
+          pair_product(tm_d, a, pp, idesc);
+          umma_commit(done);
+        }
+        if (k > 0) {
+          pair_product(tm_q, q, pp, idesc);
+          umma_commit(done_q);
+        }
+        if (k < p.steps - 1) {
+          if (!wait_ready()) break;                 // A_k P_k
+          pair_product(tm_d, a, pp, idesc);
+          umma_commit(done);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ||X||^2 is the trace; summed over a warp's rows, then over the warps in turn
+    float d = 0.f;
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      if (col0 + j == row) d = acc[j];
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) trace[warp - 2] = d;
+    epilogue_sync();
+    d = 0.f;
+    for (int i = 0; i < 8; ++i) d += trace[i];
+    const float norm = sqrtf(d) + p.eps;
+    scale = norm > 0.f ? 1.f / norm : (norm == 0.f ? 0.f : norm);   // zeros stay zeros, NaN stays NaN
+#pragma unroll
+    for (int j = 0; j < 64; ++j) acc[j] = acc[j] * scale * scale;
+
+    auto publish = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bar);
+    };
+    // the thread's 64 values of an r x r operand, f(j) of column col0 + j, times 2^e
+    auto write_f16 = [&](uint8_t* to, auto f) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float v[32];
+        f(g, v);
+        store_split<false>(to + ch, row, 4 * g, v);
+      }
+    };
+    auto write_q = [&](auto f) {                    // the final Q, in X's type
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float v[32];
+        f(g, v);
+        store_split<BF16>(sm_q + ch, row, 4 * g, v);
+      }
+    };
+    int n_done = 0, n_done_q = 0;
+    auto wait_done = [&] {
+      const bool ok = mbar_wait(done, n_done++ & 1, err);
+      tc_fence_after();
+      return ok;
+    };
+    auto wait_done_q = [&] {
+      const bool ok = mbar_wait(done_q, n_done_q++ & 1, err);
+      tc_fence_after();
+      return ok;
+    };
+    const float f_last = exp2i(p.eq_last);
+    bool ok = true;
+    if (p.steps == 0)
+      write_q([&](int g, float (&v)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = row == col0 + 32 * g + j ? f_last : 0.f;
+      });
+    for (int k = 0; k < p.steps && ok; ++k) {
+      const bool last = k == p.steps - 1;
+      const float fa = exp2i(p.ea);
+      write_f16(sm_a, [&](int g, float (&v)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = acc[32 * g + j] * fa;
+      });
+      publish(ready);
+      // P = a I + b A + c A^2
+      if (!(ok = wait_done())) break;
+      const float fc = p.c * exp2i(-2 * p.ea), fp = exp2i(p.eb);
+      auto poly = [&](int g, float f, float (&v)[32]) {
+        tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float diag = row == col0 + 32 * g + j ? p.a : 0.f;
+          v[j] = fmaf(fc, v[j], fmaf(p.b, acc[32 * g + j], diag)) * f;
+        }
+      };
+      if (!(last && k == 0)) write_f16(sm_p, [&](int g, float (&v)[32]) { poly(g, fp, v); });
+      if (k == 0 && !last) write_f16(sm_q, [&](int g, float (&v)[32]) { poly(g, exp2i(p.eq[0]), v); });
+      if (k == 0 && last) write_q([&](int g, float (&v)[32]) { poly(g, f_last, v); });
+      publish(ready);
+      if (!last) {
+        // A P replaces A
+        if (!(ok = wait_done())) break;
+        const float ft = exp2i(-p.eb);
+        write_f16(sm_a, [&](int g, float (&v)[32]) {
+          tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= ft;
+        });
+        publish(ready);
+      }
+      if (k > 0) {
+        if (!(ok = wait_done_q())) break;
+        auto product = [&](int g, float f, float (&v)[32]) {
+          tmem_ld32(tm_q + lanes + col0 + 32 * g, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= f;
+        };
+        if (last)
+          write_q([&](int g, float (&v)[32]) { product(g, exp2i(p.eq_last - p.eq[k - 1] - p.eb), v); });
+        else
+          write_f16(sm_q, [&](int g, float (&v)[32]) { product(g, exp2i(p.eq[k] - p.eq[k - 1] - p.eb), v); });
+      }
+      if (!last) {
+        if (!(ok = wait_done())) break;
+        const float fn = exp2i(-p.ea - p.eb);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float v[32];
+          tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[32 * g + j] = v[j] * fn;
+        }
+      }
+    }
+    publish(q_ready);
+    scale *= exp2i(-p.eq_last);
+  }
+
+  // ------------------------------------------------------------ O = s Q X
+  if (warp == 0) {
+    if (lane == 0 && mbar_wait(q_ready, 0, err)) produce(1);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(kSide, kSide, BF16, 1);
+      const uint32_t q = smem_u32(sm_q);
+      bool ok = mbar_wait(q_ready, 0, err);
+      tc_fence_after();
+      for (int i = 0; i < count && ok; ++i) {
+        const int slot = i % kRing;
+        ok = (i < 2 || mbar_wait(&tempty[2 + (i & 1)], ((i >> 1) - 1) & 1, err)) &&
+             mbar_wait(&full[kRing + slot], (i / kRing) & 1, err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+        for (int part = 0; part < 2; ++part) {      // Q's hi, then its lo
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // the left operand K-major, the right one MN-major, both as stored
+            const uint32_t left = p.tall ? x : q + part * kSliceBytes, right = p.tall ? q + part * kSliceBytes : x;
+            umma_f16(tmem + (i & 1) * kSide, sdesc_sw128(left + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
+                     sdesc_sw128(right + k * 2048, kChunkBytes, 1024), idesc, (part | k) != 0);
+          }
+        }
+        umma_commit(&tfull[2 + (i & 1)]);
+      }
+      // no MMA may still write TMEM when the CTA frees it
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // each warp writes its 32 rows x 64 columns over the slice it came from
+    // (whose products are done) and stores that box itself
+    for (int i = 0; i < count; ++i) {
+      if (!mbar_wait(&tfull[2 + (i & 1)], (i >> 1) & 1, err)) break;
+      tc_fence_after();
+      uint8_t* box = smem + (i % kRing) * kSliceBytes + ch;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float v[32];
+        tmem_ld32(tmem + lanes + (i & 1) * kSide + col0 + 32 * g, v);
+        if (g == 1) {
+          tc_fence_before();
+          mbar_arrive(&tempty[2 + (i & 1)]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = pack_16<BF16>(v[8 * q + 2 * j] * scale, v[8 * q + 2 * j + 1] * scale);
+          *reinterpret_cast<uint4*>(box + row_piece(row, 4 * g + q)) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int at = (first + i) * kSide;
+        const int x0 = p.tall ? col0 : at + col0, y0 = p.tall ? at + quarter * 32 : quarter * 32;
+        if (x0 < p.cols && y0 < p.rows) tma_store_3d(&omap, box + quarter * 4096, x0, y0, matrix);
+        bulk_commit();
+        if (i > 0) {                                // the previous slice's box has been read
+          bulk_wait_read<1>();
+          mbar_arrive(&empty[kRing + (i - 1) % kRing]);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && *err) atomicOr(&g_orth_timeout, 1);
+}
+
+// Copies a stack whose rows TMA cannot address to one whose rows it can, or back.
+__global__ void __launch_bounds__(256)
+    copy_stack_kernel(const uint16_t* from, int64_t from_stride, int64_t from_ld, uint16_t* to, int64_t to_stride,
+                      int64_t to_ld, int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t total = batch * rows * cols, step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
+    const int64_t r = i / cols, c = i - r * cols, b = r / rows;
+    const int64_t y = r - b * rows;
+    to[b * to_stride + y * to_ld + c] = from[b * from_stride + y * from_ld + c];
+  }
+}
+
+muonh_status orth_fail(muonh_status st, const char* msg) {
+  set_error_message(msg);
+  return st;
+}
+
+// Rows of a 16-bit stack that TMA can address: 16-byte aligned base and strides.
+bool tma_stack(const void* p, int64_t stride, int64_t ld, int64_t batch, int64_t rows) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows == 1 || (ld % 8 == 0 && ld > 0)) &&
+         (batch == 1 || (stride % 8 == 0 && stride > 0));
+}
+
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+struct Stack {
+  void* p;
+  int64_t stride, ld;
+};
+
+bool encode_stack(CUtensorMap* map, const Stack& s, const muonh_orthogonalize_desc& d, int box_rows) {
+  // strides that no coordinate uses still have to be valid ones
+  const int64_t ld = d.rows == 1 ? up8(d.cols) : s.ld, stride = d.batch == 1 ? up8(ld * d.rows) : s.stride;
+  return encode_tiled_stack(map, s.p, d.dtype == MUONH_DTYPE_BF16, d.cols, d.rows, d.batch, ld, stride, box_rows);
+}
+
+muonh_status check_orth(const muonh_orthogonalize_desc* d) {
+  if (!d) return orth_fail(MUONH_ERR_INVALID_ARG, "desc is NULL");
+  if (d->batch < 0 || d->rows < 0 || d->cols < 0 || d->batch > (1 << 24) || d->rows > (1 << 30) || d->cols > (1 << 30))
+    return orth_fail(MUONH_ERR_INVALID_ARG, "batch must be in [0, 2^24], rows and cols in [0, 2^30]");
+  if (d->dtype != MUONH_DTYPE_BF16 && d->dtype != MUONH_DTYPE_F16)
+    return orth_fail(MUONH_ERR_INVALID_ARG, "dtype must be MUONH_DTYPE_BF16 or MUONH_DTYPE_F16");
+  if (d->ns_steps < 0 || d->ns_steps > kMaxSteps) return orth_fail(MUONH_ERR_INVALID_ARG, "ns_steps must be in [0, 16]");
+  if (!std::isfinite(d->ns_a) || !std::isfinite(d->ns_b) || !std::isfinite(d->ns_c) || !std::isfinite(d->eps) ||
+      d->eps < 0.f)
+    return orth_fail(MUONH_ERR_INVALID_ARG, "the coefficients must be finite and eps finite and >= 0");
+  if (std::min(d->rows, d->cols) > kSide)
+    return orth_fail(MUONH_ERR_UNSUPPORTED, "the smaller side of a matrix must be at most 128");
+  if (d->batch == 0 || d->rows == 0 || d->cols == 0) return MUONH_OK;
+  if (!d->x || !d->out) return orth_fail(MUONH_ERR_INVALID_ARG, "x or out is NULL");
+  if ((d->rows > 1 && (d->ldx < d->cols || d->ldo < d->cols)) || d->x_stride < 0 || d->out_stride < 0)
+    return orth_fail(MUONH_ERR_INVALID_ARG, "row strides must be at least cols, matrix strides at least 0");
+  if ((reinterpret_cast<uintptr_t>(d->x) | reinterpret_cast<uintptr_t>(d->out)) & 1)
+    return orth_fail(MUONH_ERR_ALIGNMENT, "x and out must be 2-byte aligned");
+  return MUONH_OK;
+}
+
+size_t copy_bytes(const muonh_orthogonalize_desc& d) {
+  return static_cast<size_t>(d.batch) * d.rows * up8(d.cols) * 2;
+}
+
+}  // namespace
+}  // namespace muonh
+
+using namespace muonh;
+
+extern "C" size_t muonh_orthogonalize_workspace(const muonh_orthogonalize_desc* d) {
+  if (!d || d->batch < 1 || d->rows < 1 || d->cols < 1) return 0;
+  size_t n = 0;
+  if (!tma_stack(d->x, d->x_stride, d->ldx, d->batch, d->rows)) n += copy_bytes(*d);
+  if (!tma_stack(d->out, d->out_stride, d->ldo, d->batch, d->rows)) n += copy_bytes(*d);
+  return n;
+}
+
+extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  set_error_message("");
+  if (const muonh_status st = check_orth(d)) return st;
+  if (d->batch == 0 || d->rows == 0 || d->cols == 0) return MUONH_OK;
+  if (workspace_bytes < muonh_orthogonalize_workspace(d) || (muonh_orthogonalize_workspace(d) && !workspace))
+    return orth_fail(MUONH_ERR_INVALID_ARG, "the workspace is smaller than muonh_orthogonalize_workspace says");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15)
+    return orth_fail(MUONH_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+
+  const int64_t ld = up8(d->cols), copies = std::min<int64_t>((d->batch * d->rows * d->cols + 255) / 256, 16ll * sms);
+  Stack in{const_cast<void*>(d->x), d->x_stride, d->ldx}, out{d->out, d->out_stride, d->ldo};
+  uint8_t* work = static_cast<uint8_t*>(workspace);
+  if (!tma_stack(in.p, in.stride, in.ld, d->batch, d->rows)) {
+    copy_stack_kernel<<<static_cast<unsigned>(copies), 256, 0, s>>>(
+        static_cast<const uint16_t*>(in.p), in.stride, in.ld, reinterpret_cast<uint16_t*>(work), ld * d->rows, ld,
+        d->batch, d->rows, d->cols);
+    in = Stack{work, ld * d->rows, ld};
+    work += copy_bytes(*d);
+  }
+  const bool copy_back = !tma_stack(out.p, out.stride, out.ld, d->batch, d->rows);
+  if (copy_back) out = Stack{work, ld * d->rows, ld};
+
+  OrthParams p{};
+  p.tall = d->rows > d->cols;
+  p.rows = static_cast<int32_t>(d->rows);
+  p.cols = static_cast<int32_t>(d->cols);
+  p.slices = static_cast<int32_t>((std::max(d->rows, d->cols) + kSide - 1) / kSide);
+  p.steps = d->ns_steps;
+  p.a = d->ns_a;
+  p.b = d->ns_b;
+  p.c = d->ns_c;
+  p.eps = d->eps;
+  ns_chain_scales(p.a, p.b, p.c, p.steps, &p.ea, &p.eb, p.eq);
+  p.eq_last = (d->dtype == MUONH_DTYPE_BF16 || p.steps == 0) ? 0 : p.eq[p.steps - 1];
+  // more CTAs per matrix while that leaves none of them waiting for an SM and
+  // each has two slices at least
+  int ranks = 1;
+  while (ranks < kMaxCluster && d->batch * ranks * 2 <= sms && p.slices >= 4 * ranks) ranks *= 2;
+
+  CUtensorMap xmap, omap;
+  if (!encode_stack(&xmap, in, *d, kSide) || !encode_stack(&omap, out, *d, 32))
+    return orth_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(d->batch * ranks));
+  cfg.blockDim = dim3(kOrthThreads);
+  cfg.dynamicSmemBytes = kOrthSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const bool bf16 = d->dtype == MUONH_DTYPE_BF16;
+  cudaError_t e = bf16 ? cudaFuncSetAttribute(orthogonalize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kOrthSmem)
+                       : cudaFuncSetAttribute(orthogonalize_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kOrthSmem);
+  if (e == cudaSuccess)
+    e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
+             : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);
+  if (e == cudaSuccess && copy_back) {
+    copy_stack_kernel<<<static_cast<unsigned>(copies), 256, 0, s>>>(
+        static_cast<const uint16_t*>(out.p), out.stride, out.ld, static_cast<uint16_t*>(d->out), d->out_stride, d->ldo,
+        d->batch, d->rows, d->cols);
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return orth_fail(MUONH_ERR_CUDA, "launch of the orthogonalize kernel failed");
+  return MUONH_OK;
+}
+
+cudaError_t muonh::take_orth_timeout(int* flag, cudaStream_t s) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_orth_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbolAsync(g_orth_timeout, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e;
+}

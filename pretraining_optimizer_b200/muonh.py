@@ -27,6 +27,7 @@ EXPORTED_SYMBOLS = (
     "muonh_enable_timing", "muonh_phase_times", "muonh_phase_flops", "muonh_momentum_norm_noalloc",
     "muonh_average",
     "muonh_adamw_step", "muonh_layer_norm", "muonh_layer_norm_workspace", "muonh_layer_norm_backward",
+    "muonh_orthogonalize", "muonh_orthogonalize_workspace", "muonh_operator_status",
     "muonh_check_wait_timeout", "muonh_destroy", "muonh_status_string", "muonh_last_error",
 )
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
@@ -60,6 +61,13 @@ class AdamWTensor(Structure):
 class AdamWConfig(Structure):
     _fields_ = [("lr", c_float), ("beta1", c_float), ("beta2", c_float), ("eps", c_float),
                 ("weight_decay", c_float)]
+
+
+class OrthogonalizeDesc(Structure):
+    _fields_ = [("x", c_void_p), ("out", c_void_p), ("batch", c_int64), ("rows", c_int64), ("cols", c_int64),
+                ("x_stride", c_int64), ("ldx", c_int64), ("out_stride", c_int64), ("ldo", c_int64),
+                ("dtype", c_int32), ("ns_steps", c_int32), ("ns_a", c_float), ("ns_b", c_float),
+                ("ns_c", c_float), ("eps", c_float)]
 
 
 class MuonHError(RuntimeError):
@@ -109,6 +117,10 @@ def library() -> ctypes.CDLL:
     lib.muonh_layer_norm_backward.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                               c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64, c_int32,
                                               c_void_p, c_size_t, c_void_p]
+    lib.muonh_orthogonalize.argtypes = [POINTER(OrthogonalizeDesc), c_void_p, c_size_t, c_void_p]
+    lib.muonh_orthogonalize_workspace.argtypes = [POINTER(OrthogonalizeDesc)]
+    lib.muonh_orthogonalize_workspace.restype = c_size_t
+    lib.muonh_operator_status.argtypes = [c_void_p]
     lib.muonh_check_wait_timeout.argtypes = [ctypes.c_double, c_void_p]
     lib.muonh_destroy.argtypes = [c_void_p]
     lib.muonh_destroy.restype = None
@@ -120,7 +132,7 @@ def library() -> ctypes.CDLL:
                  "muonh_export_state", "muonh_import_state", "muonh_device_status",
                  "muonh_enable_timing", "muonh_phase_times", "muonh_phase_flops", "muonh_momentum_norm_noalloc",
                  "muonh_average", "muonh_adamw_step", "muonh_check_wait_timeout", "muonh_layer_norm",
-                 "muonh_layer_norm_backward"):
+                 "muonh_layer_norm_backward", "muonh_orthogonalize", "muonh_operator_status"):
         getattr(lib, name).restype = c_int32
     _LIB = lib
     return lib

@@ -1,4 +1,5 @@
-"""ctypes bindings of the operators around the update: layer norm.
+"""ctypes bindings of the operators around the update: layer norm, and
+orthogonalising stacks of matrices.
 
 Like the rest of the binding these calls check and marshal arguments; the work
 is in the library's CUDA kernels.  Each call runs on the device of its tensors,
@@ -8,8 +9,9 @@ that results and scratch are allocated on, as under `torch.cuda.stream(stream)`.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
-from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, _check, library
+from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, OrthogonalizeDesc, _check, library
 
 
 def _dtype_code(dtype):
@@ -139,3 +141,52 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
             None if dbias is None else dbias.data_ptr(), rows, n, _dtype_code(x.dtype),
             None if work is None else work.data_ptr(), size, handle))
     return dx, dweight, dbias
+
+
+def _stack(t, what: str):
+    """(pointer, matrix stride, row stride) of a 2-D or 3-D tensor as a stack of matrices."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    if t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"{what} must have rows that do not overlap")
+    return t.data_ptr(), t.stride(0) if t.dim() == 3 else 0, max(t.stride(-2), t.shape[-1])
+
+
+def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, stream=None):
+    """The Newton-Schulz output of each matrix of a stack x ([rows, cols] or
+    [batch, rows, cols], bf16 or fp16, unit column stride, any other strides),
+    for matrices whose smaller side is at most 128: one Muon update per
+    attention head.  Returns a tensor of x's shape and type, or `out`, which
+    may be x."""
+    import torch
+    _tensor(x, "x", (torch.bfloat16, torch.float16))
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be a matrix or a stack of matrices")
+    xp, xs, ldx = _stack(x, "x")
+    a, b, c = ns_coeffs
+    rows, cols = x.shape[-2:]
+    lib = library()
+    with _on(x.device, stream) as handle:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _tensor(out, "out", (x.dtype,), x.device)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+        op, os_, ldo = _stack(out, "out")
+        if x.dim() == 3 and x.shape[0] > 1 and os_ < cols:
+            raise ValueError("out must have matrices that do not overlap")
+        d = OrthogonalizeDesc(xp, op, x.shape[0] if x.dim() == 3 else 1, rows, cols, xs, ldx, os_, ldo,
+                              _dtype_code(x.dtype), int(ns_steps), a, b, c, eps)
+        size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))
+        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+        _check(lib.muonh_orthogonalize(ctypes.byref(d), None if work is None else work.data_ptr(), size, handle))
+    return out
+
+
+def operator_status(stream=None) -> None:
+    """Synchronises `stream` (default: the current one) and raises MuonHError
+    if a device wait gave up in an operator call since the previous check."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    _check(library().muonh_operator_status(stream.cuda_stream))

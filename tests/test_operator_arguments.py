@@ -71,3 +71,66 @@ def test_row_views():
     for bad in (x[:, :3], x[:, :, ::2], x.transpose(0, 1), x[:1, :1].expand(6, 4, 10), x[0, 0].expand(4, 10)):
         with pytest.raises(ValueError):
             _rows(bad, "x")
+
+
+def _orth(**kw):
+    from pretraining_optimizer_b200.muonh import OrthogonalizeDesc
+    ok = dict(x=A, out=A, batch=2, rows=32, cols=64, x_stride=2048, ldx=64, out_stride=2048, ldo=64, dtype=1,
+              ns_steps=5, ns_a=3.4445, ns_b=-4.775, ns_c=2.0315, eps=1e-7)
+    return OrthogonalizeDesc(*{**ok, **kw}.values())
+
+
+def test_orthogonalize_checks():
+    lib = P.library()
+
+    def call(work=None, size=0, **kw):
+        return lib.muonh_orthogonalize(ctypes.byref(_orth(**kw)), work, size, None)
+
+    assert lib.muonh_orthogonalize(None, None, 0, None) == 1
+    assert call(batch=-1) == 1 and call(rows=-1) == 1 and call(cols=-1) == 1 and call(batch=2 ** 25) == 1
+    assert call(dtype=0) == 1 and call(dtype=9) == 1
+    assert call(ns_steps=-1) == 1 and call(ns_steps=17) == 1
+    assert call(ns_a=float("nan")) == 1 and call(eps=-1e-9) == 1 and call(eps=float("inf")) == 1
+    assert call(rows=129, cols=129, ldx=136, ldo=136) == 6 and b"128" in lib.muonh_last_error()
+    assert call(x=None) == 1 and call(out=None) == 1
+    assert call(ldx=63) == 1 and call(ldo=8) == 1 and call(x_stride=-8) == 1
+    assert call(x=A + 1) == 2
+    assert call(batch=0, x=None, out=None) == 0 and call(rows=0) == 0 and call(cols=0) == 0
+
+
+def test_orthogonalize_workspace():
+    lib = P.library()
+
+    def size(**kw):
+        return lib.muonh_orthogonalize_workspace(ctypes.byref(_orth(**kw)))
+
+    one = 2 * 32 * 64 * 2
+    assert size() == 0 and size(batch=0) == 0
+    assert size(x=A + 2) == one and size(ldx=65, x_stride=2080) == one and size(x_stride=2049) == one
+    assert size(x_stride=0) == one                          # the same matrix twice
+    assert size(ldx=65, ldo=65, x_stride=2080, out_stride=2080) == 2 * one
+    assert size(cols=61, ldx=61, x_stride=32 * 61, ldo=64) == one
+    assert size(batch=1, x_stride=3) == 0 and size(rows=1, ldx=67, ldo=65) == 0
+    assert lib.muonh_orthogonalize_workspace(None) == 0
+    d = _orth(x=A + 2)
+    assert lib.muonh_orthogonalize(ctypes.byref(d), None, one, None) == 1
+    assert lib.muonh_orthogonalize(ctypes.byref(d), A, one - 1, None) == 1
+    assert lib.muonh_orthogonalize(ctypes.byref(d), A + 8, one, None) == 2
+
+
+def test_orthogonalize_layout():
+    from pretraining_optimizer_b200.muonh import OrthogonalizeDesc as D
+    assert ctypes.sizeof(D) == 96 and D.x_stride.offset == 40 and D.dtype.offset == 72 and D.eps.offset == 92
+
+
+def test_orthogonalize_binding_rejects():
+    import torch
+    with pytest.raises(TypeError):
+        P.orthogonalize(torch.zeros(4, 8, dtype=torch.bfloat16))
+    from pretraining_optimizer_b200.operators import _stack
+    x = torch.zeros(3, 6, 10)
+    assert _stack(x, "x")[1:] == (60, 10) and _stack(x[:, :, 2:7], "x")[1:] == (60, 10)
+    assert _stack(x[1], "x")[1:] == (0, 10) and _stack(x.transpose(0, 1), "x")[1:] == (10, 60)
+    for bad in (x.mT, x[:, :, ::2], x[:, :1].expand(3, 6, 10)):
+        with pytest.raises(ValueError):
+            _stack(bad, "x")
