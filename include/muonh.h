@@ -427,6 +427,48 @@ size_t muonh_orthogonalize_workspace(const muonh_orthogonalize_desc* desc);
 muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* desc, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/* Quantise to 8 bits with a power-of-two scale per block of 128 (the recipe's
+ * blockwise e4m3: 1 x 128 groups for activations and gradients, 128 x 128
+ * blocks for weights, E8M0 scales).  For a block with largest magnitude m,
+ *   k = the smallest integer >= -127 with m <= 448 2^k  (0 for zeros)
+ *   q = x 2^-k rounded to e4m3 (ties to even);  scale byte = k + 127.
+ * A block that holds NaN or Inf gets scale byte 255 (NaN) and NaN throughout.
+ *   x           rows x cols of dtype (MUONH_DTYPE_*), row stride ldx.
+ *   block_rows  1: groups of 128 along each row; 128: 128 x 128 blocks.
+ *   q, scale    NULL, or rows x cols bytes (row stride ldq, a multiple of 16,
+ *               16-byte aligned) and ceil(rows / block_rows) x ceil(cols / 128)
+ *               scale bytes (row stride ld_scale, any alignment).
+ *   qt, scale_t NULL, or the same for the transpose of x: cols x rows bytes and
+ *               ceil(cols / block_rows) x ceil(rows / 128) scale bytes.  Its
+ *               groups run along the rows of the transpose, down x's columns.
+ * At least one orientation is needed; both come from one read of x.  Bytes
+ * between a row's end and its stride are left as they were. */
+muonh_status muonh_block_quantize(const void* x, int64_t ldx, int64_t rows, int64_t cols, int32_t dtype,
+                                  int32_t block_rows, void* q, int64_t ldq, uint8_t* scale, int64_t ld_scale,
+                                  void* qt, int64_t ldqt, uint8_t* scale_t, int64_t ld_scale_t, void* stream);
+
+/* An operand of muonh_block_matmul, as muonh_block_quantize writes it. */
+typedef struct {
+  const void* q;            /* rows x k e4m3 bytes, 16-byte aligned rows       */
+  const uint8_t* scale;     /* ceil(rows / block_rows) x ceil(k / 128) bytes   */
+  int64_t rows;
+  int64_t ld;               /* row stride of q in bytes, a multiple of 16      */
+  int64_t ld_scale;         /* row stride of scale in bytes                    */
+  int32_t block_rows;       /* 1 or 128: rows that share a scale               */
+  int32_t pad_;
+} muonh_block_operand;
+
+/* D = A B^T for block-scaled 8-bit operands, D[a->rows, b->rows]: a linear
+ * layer's forward product (x, W), its activation gradient (dy, W transposed) and
+ * its weight gradient (dy transposed, x transposed).
+ *   d           row stride ldd elements of dtype (MUONH_DTYPE_*), overwritten;
+ *               with accumulate != 0 (fp32 only) the product is added to it.
+ *               Must not overlap the operands.
+ * Products are accumulated in fp32 and rounded once to dtype.  k == 0 gives
+ * zeros (or leaves an accumulated d as it is). */
+muonh_status muonh_block_matmul(const muonh_block_operand* a, const muonh_block_operand* b, int64_t k, void* d,
+                                int64_t ldd, int32_t dtype, int32_t accumulate, void* stream);
+
 /* MUONH_ERR_TIMEOUT if a device wait gave up in an operator call above since
  * the previous call (then clears the record), else OK; synchronises `stream`,
  * which must be the one, or ordered after the ones, that the calls ran on. */

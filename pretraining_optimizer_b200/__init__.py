@@ -12,5 +12,5 @@ from .muonh import (  # noqa: F401
     average, adamw_step, check_wait_timeout,
 )
 from .operators import (  # noqa: F401
-    layer_norm, layer_norm_backward, operator_status, orthogonalize,
+    block_matmul, block_quantize, block_quantize_weight, layer_norm, layer_norm_backward, operator_status, orthogonalize,
 )

@@ -236,12 +236,25 @@ bool muonh::encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool muonh::encode_bytes(CUtensorMap* out, void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" muonh_status muonh_operator_status(void* stream) {
   set_error_message("");
-  int gave_up = 0;
-  if (take_orth_timeout(&gave_up, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  int orth = 0, block = 0;
+  if (take_orth_timeout(&orth, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      take_block_timeout(&block, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return fail(MUONH_ERR_CUDA, "reading the operators' status failed");
-  if (gave_up) return fail(MUONH_ERR_TIMEOUT, "a device-side bounded wait gave up");
+  if (orth || block) return fail(MUONH_ERR_TIMEOUT, "a device-side bounded wait gave up");
   return MUONH_OK;
 }
 

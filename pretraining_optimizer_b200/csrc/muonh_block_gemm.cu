@@ -1,0 +1,498 @@
+// Products of 8-bit matrices with a power-of-two scale per block of 128
+// (sm_100a): D = A B^T, the forward, activation-gradient and weight-gradient
+// products of the recipe's linear layers (Puro-2B report: blockwise e4m3).
+//
+//   D[m, n] (+)= sum over k-blocks b of 2^(sa[m, b] + sb[n, b] - 254)
+//                                       sum_{k in b} qa[m, k] qb[n, k]
+// The tensor cores take the scales themselves: tcgen05.mma kind::mxf8f6f4
+// multiplies blocks of 32 along k by a pair of E8M0 scales, so a block of 128 is
+// four MMAs that use the same scale byte.  A 32-bit TMEM word per row holds the
+// bytes of four k-blocks (512 of k); the instruction descriptor picks the byte.
+//
+// One persistent CTA per SM computes 128 x BN tiles (BN = 256 where there are
+// enough tiles).  Warp 0 loads operands by TMA (one k-block of 128 bytes is one
+// 128-byte swizzled row), warp 2 gathers the scale words of both operands into
+// shared memory, warp 1 copies them to TMEM (tcgen05.cp) and issues the MMAs,
+// and warps 4 to 11 drain the accumulator, round once and store.
+//
+// The tensor cores' fp32 accumulation truncates, with an error that grows with
+// the number of products added up.  fp32 results are therefore accumulated
+// over at most kChunkBlocks k-blocks in TMEM, and the chunks are added in IEEE
+// fp32 in the result itself, by the thread that wrote it.
+#include <algorithm>
+
+#include "muonh_common.cuh"
+
+namespace muonh {
+namespace {
+
+constexpr int kTm = 128;                         // tile rows
+constexpr int kKBlock = 128;                     // k per stage: one scale block
+constexpr int kThreads = 384;
+constexpr int kEpi = 256;                        // epilogue threads
+constexpr int kScaleRing = 4;                    // scale words in flight: 512 of k each
+constexpr int kChunkBlocks = 8;                  // fp32 results: k-blocks per TMEM accumulation
+
+template <int BN>
+struct BlockCfg {
+  static constexpr int kABytes = kTm * kKBlock;
+  static constexpr int kBBytes = BN * kKBlock;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kAccs = BN == 256 ? 1 : 2;      // accumulators in TMEM, next to the scales
+  static constexpr int kScaleBlocks = 1 + (BN + 127) / 128;   // 512-byte blocks of scale words: A, and B per 128 rows
+  static constexpr int kScaleBytes = kScaleBlocks * 512;
+  static constexpr int kScaleOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kScaleOffset + kScaleRing * kScaleBytes;
+  static constexpr int kSmem = kBarOffset + 512 + 1024;
+  static constexpr uint32_t kScaleCol = 256;           // first TMEM column of the scale words
+  static_assert(kSmem <= 227 * 1024, "shared memory of the block-scaled kernel exceeds 227 KB");
+};
+
+__device__ int g_block_timeout;                  // a wait gave up in some call since the flag was read
+
+struct BlockParams {
+  const uint8_t* sa;
+  const uint8_t* sb;
+  int64_t ld_sa, ld_sb;
+  int32_t sa_shift, sb_shift;                    // 7: one scale per 128 rows, 0: one per row
+  int32_t sa_words, sb_words;                    // scales can be read four at a time
+  void* d;
+  int64_t ldd;
+  int32_t m, n, k_blocks;
+  int32_t dtype, accumulate, wide_store;
+  int32_t tiles_m, tiles_n, band;
+};
+
+// D[tmem] (+)= (A 2^sa) (B 2^sb)^T over 32 of k, e4m3 operands with E8M0 scales.
+__device__ __forceinline__ void umma_mxf8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
+                                          uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
+// 32 rows of 16 bytes from shared memory to 4 TMEM columns of lanes 0..31, repeated for the other three lane groups.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Descriptor of that 512-byte block: no swizzle, 8 rows of 16 bytes per 128 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Instruction descriptor, kind::mxf8f6f4: both operands e4m3 and K-major, E8M0
+// scales, byte `id` of the scale words.
+__device__ __forceinline__ uint32_t idesc_mxf8(int m, int n, int id) {
+  return (static_cast<uint32_t>(id) << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(id) << 29);
+}
+
+// Tile t of the walk: bands of `band` tile rows, column by column within a
+// band, so that the tiles in flight share operands in L2.
+__device__ __forceinline__ void tile_at(const BlockParams& p, int64_t t, int& tm, int& tn) {
+  const int64_t per_band = static_cast<int64_t>(p.band) * p.tiles_n;
+  const int b = static_cast<int>(t / per_band);
+  const int rows = min(p.band, p.tiles_m - b * p.band);
+  const int r = static_cast<int>(t - b * per_band);
+  tm = b * p.band + r % rows;
+  tn = r / rows;
+}
+
+// Scale bytes of k-blocks 4 g .. 4 g + 3 of one operand row, as one word; 2^0
+// where there is no row or no such block (what they scale is zero).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int shift, int words, int row, int rows,
+                                               int g, int k_blocks) {
+  if (row >= rows) return 0x7f7f7f7fu;
+  const uint8_t* p = s + static_cast<int64_t>(row >> shift) * ld + 4 * g;
+  if (words && 4 * g + 4 <= k_blocks) return __ldg(reinterpret_cast<const uint32_t*>(p));
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= static_cast<uint32_t>(4 * g + i < k_blocks ? __ldg(p + i) : 127) << (8 * i);
+  return w;
+}
+
+struct alignas(32) Vec32 {
+  uint32_t u[8];
+};
+__device__ __forceinline__ void store32(void* p, const Vec32& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.u[0]), "r"(v.u[1]),
+               "r"(v.u[2]), "r"(v.u[3]), "r"(v.u[4]), "r"(v.u[5]), "r"(v.u[6]), "r"(v.u[7])
+               : "memory");
+}
+
+// 32 results of one row.  `add`: fp32 results are added to what is there.
+__device__ __forceinline__ void store_row(const BlockParams& p, int row, int col, float (&v)[32], bool add) {
+  if (row >= p.m || col >= p.n) return;
+  if (p.dtype == MUONH_DTYPE_F32) {
+    float* d = static_cast<float*>(p.d) + static_cast<int64_t>(row) * p.ldd + col;
+    if (p.wide_store && col + 32 <= p.n) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        Vec32 o;
+        if (add) {
+          const float4 x = reinterpret_cast<const float4*>(d)[2 * q], y = reinterpret_cast<const float4*>(d)[2 * q + 1];
+          v[8 * q] += x.x, v[8 * q + 1] += x.y, v[8 * q + 2] += x.z, v[8 * q + 3] += x.w;
+          v[8 * q + 4] += y.x, v[8 * q + 5] += y.y, v[8 * q + 6] += y.z, v[8 * q + 7] += y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.u[j] = __float_as_uint(v[8 * q + j]);
+        store32(d + 8 * q, o);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j < p.n) d[j] = add ? d[j] + v[j] : v[j];
+    }
+    return;
+  }
+  const bool bf16 = p.dtype == MUONH_DTYPE_BF16;
+  uint32_t u[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (bf16) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      u[j] = *reinterpret_cast<uint32_t*>(&h);
+    } else {
+      __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+      u[j] = *reinterpret_cast<uint32_t*>(&h);
+    }
+  }
+  uint16_t* d = static_cast<uint16_t*>(p.d) + static_cast<int64_t>(row) * p.ldd + col;
+  if (p.wide_store && col + 32 <= p.n) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      Vec32 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o.u[j] = u[8 * q + j];
+      store32(d + 16 * q, o);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (col + j < p.n) d[j] = static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    block_matmul_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap amap,
+                        const __grid_constant__ CUtensorMap bmap) {
+  using C = BlockCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* sfull = empty + C::kStages;
+  uint64_t* sempty = sfull + kScaleRing;
+  uint64_t* tfull = sempty + kScaleRing;
+  uint64_t* tempty = tfull + C::kAccs;
+  uint64_t* drain = tempty + C::kAccs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* err = reinterpret_cast<int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kScaleRing; ++s) {
+      mbar_init(&sfull[s], 32);
+      mbar_init(&sempty[s], 1);
+    }
+    for (int a = 0; a < C::kAccs; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kEpi);
+    }
+    mbar_init(drain, 1);
+    *err = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // every role walks over the same (tile, chunk of k) sequence
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const int chunk = p.dtype == MUONH_DTYPE_F32 ? kChunkBlocks : p.k_blocks;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      int64_t i = 0;                             // k-blocks issued
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        int tm, tn;
+        tile_at(p, t, tm, tn);
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++i) {
+          const int s = static_cast<int>(i % C::kStages);
+          if (i >= C::kStages && !mbar_wait(&empty[s], static_cast<uint32_t>(i / C::kStages - 1) & 1, err)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&full[s], C::kStageBytes);
+          uint8_t* dst = smem + s * C::kStageBytes;
+          tma_load_2d(dst, &amap, &full[s], kb * kKBlock, tm * kTm);
+          tma_load_2d(dst + C::kABytes, &bmap, &full[s], kb * kKBlock, tn * BN);
+        }
+      }
+      // copies in flight land before the CTA may exit
+      for (int64_t j = std::max<int64_t>(0, i - C::kStages); j < i; ++j) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1) &&
+               globaltimer() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int64_t i = 0, g = 0, work = 0;            // k-blocks, scale words and accumulators used
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++i) {
+          const int acc = static_cast<int>(work % C::kAccs);
+          if (kb % chunk == 0) {
+            if (work >= C::kAccs && !mbar_wait(&tempty[acc], static_cast<uint32_t>(work / C::kAccs - 1) & 1, err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          const int ring = static_cast<int>(g % kScaleRing);
+          const uint32_t sc = tmem + C::kScaleCol + ring * 16;
+          if ((kb & 3) == 0) {
+            // copies and MMAs of one thread run in the order that they are
+            // issued in, so the words are in place for the MMAs below and the
+            // ones that they replace have been used
+            if (!mbar_wait(&sfull[ring], static_cast<uint32_t>(g / kScaleRing) & 1, err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t from = smem_u32(smem + C::kScaleOffset + ring * C::kScaleBytes);
+#pragma unroll
+            for (int b = 0; b < C::kScaleBlocks; ++b) copy_scales(sc + 4 * b, scale_desc(from + 512 * b));
+            umma_commit(&sempty[ring]);
+          }
+          const int s = static_cast<int>(i % C::kStages);
+          if (!mbar_wait(&full[s], static_cast<uint32_t>(i / C::kStages) & 1, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
+          const uint32_t idesc = idesc_mxf8(kTm, BN, kb & 3);
+#pragma unroll
+          for (int k = 0; k < kKBlock / 32; ++k)
+            umma_mxf8(tmem + acc * 128, sdesc_sw128(a + k * 32, 16, 1024), sdesc_sw128(b + k * 32, 16, 1024), idesc,
+                      sc, sc + 4, (kb % chunk) != 0 || k != 0);
+          umma_commit(&empty[s]);
+          if ((kb & 3) == 3 || kb == p.k_blocks - 1) ++g;
+          if (kb % chunk == chunk - 1 || kb == p.k_blocks - 1) {
+            umma_commit(&tfull[acc]);
+            ++work;
+          }
+        }
+      }
+      // no MMA may still write TMEM when the CTA frees it
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // --------------------------------------------------------- scale words
+    // row r of a block of 128 is word r / 32 of the 16 bytes of TMEM lane r % 32
+    int64_t g = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      for (int w = 0; 4 * w < p.k_blocks && ok; ++w, ++g) {
+        const int ring = static_cast<int>(g % kScaleRing);
+        uint32_t u[C::kScaleBlocks][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          u[0][j] = scale_word(p.sa, p.ld_sa, p.sa_shift, p.sa_words, tm * kTm + 32 * j + lane, p.m, w, p.k_blocks);
+#pragma unroll
+        for (int b = 1; b < C::kScaleBlocks; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            u[b][j] = 128 * (b - 1) + 32 * j < BN
+                          ? scale_word(p.sb, p.ld_sb, p.sb_shift, p.sb_words, tn * BN + 128 * (b - 1) + 32 * j + lane,
+                                       p.n, w, p.k_blocks)
+                          : 0x7f7f7f7fu;
+        if (g >= kScaleRing && !mbar_wait(&sempty[ring], static_cast<uint32_t>(g / kScaleRing - 1) & 1, err)) ok = false;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        uint8_t* to = smem + C::kScaleOffset + ring * C::kScaleBytes + lane * 16;
+#pragma unroll
+        for (int b = 0; b < C::kScaleBlocks; ++b)
+          *reinterpret_cast<uint4*>(to + 512 * b) = make_uint4(u[b][0], u[b][1], u[b][2], u[b][3]);
+        fence_proxy_async_smem();
+        mbar_arrive(&sfull[ring]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    constexpr int kCols = BN / 2;                // columns per thread
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int64_t work = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      int tm, tn;
+      tile_at(p, t, tm, tn);
+      const int row = tm * kTm + quarter * 32 + lane, col = tn * BN + half * kCols;
+      for (int kb = 0; kb < p.k_blocks; kb += chunk, ++work) {
+        const int acc = static_cast<int>(work % C::kAccs);
+        if (!mbar_wait(&tfull[acc], static_cast<uint32_t>(work / C::kAccs) & 1, err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool add = kb > 0 || p.accumulate;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float v[32];
+          tmem_ld32(tmem + lanes + acc * 128 + half * kCols + c, v);
+          if (c + 32 == kCols) {
+            tc_fence_before();
+            mbar_arrive(&tempty[acc]);
+          }
+          store_row(p, row, col + c, v, add);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && *err) atomicOr(&g_block_timeout, 1);
+}
+
+// D = 0 where there is nothing to add up.
+__global__ void __launch_bounds__(256) clear_rows_kernel(uint8_t* d, int64_t pitch, int64_t bytes, int64_t rows) {
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; j < bytes; j += static_cast<int64_t>(gridDim.x) * 256)
+      d[r * pitch + j] = 0;
+}
+
+muonh_status block_fail(muonh_status st, const char* msg) {
+  set_error_message(msg);
+  return st;
+}
+
+template <int BN>
+cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(block_matmul_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             BlockCfg<BN>::kSmem);
+  if (e != cudaSuccess) return e;
+  block_matmul_kernel<BN><<<grid, kThreads, BlockCfg<BN>::kSmem, s>>>(p, a, b);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace muonh
+
+using namespace muonh;
+
+extern "C" muonh_status muonh_block_matmul(const muonh_block_operand* a, const muonh_block_operand* b, int64_t k,
+                                           void* d, int64_t ldd, int32_t dtype, int32_t accumulate, void* stream) {
+  set_error_message("");
+  if (!a || !b) return block_fail(MUONH_ERR_INVALID_ARG, "an operand is NULL");
+  if (a->rows < 0 || b->rows < 0 || k < 0 || a->rows > (1 << 30) || b->rows > (1 << 30) || k > (1 << 30))
+    return block_fail(MUONH_ERR_INVALID_ARG, "rows and k must be in [0, 2^30]");
+  if (dtype != MUONH_DTYPE_F32 && dtype != MUONH_DTYPE_BF16 && dtype != MUONH_DTYPE_F16)
+    return block_fail(MUONH_ERR_INVALID_ARG, "dtype must be a MUONH_DTYPE_* type");
+  if (accumulate && dtype != MUONH_DTYPE_F32)
+    return block_fail(MUONH_ERR_INVALID_ARG, "only fp32 results can be accumulated");
+  for (const muonh_block_operand* o : {a, b})
+    if (o->block_rows != 1 && o->block_rows != 128)
+      return block_fail(MUONH_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+  if (a->rows == 0 || b->rows == 0) return MUONH_OK;
+  if (!d || (a->rows > 1 && ldd < b->rows)) return block_fail(MUONH_ERR_INVALID_ARG, "d is NULL or its stride too small");
+  const int size = dtype == MUONH_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(d) & (size - 1)) return block_fail(MUONH_ERR_ALIGNMENT, "d is not aligned to its type");
+  const int64_t k_blocks = (k + kKBlock - 1) / kKBlock;
+  for (const muonh_block_operand* o : {a, b}) {
+    if (k == 0) break;
+    if (!o->q || !o->scale || (o->rows > 1 && o->ld < k) || (o->rows > o->block_rows && o->ld_scale < k_blocks))
+      return block_fail(MUONH_ERR_INVALID_ARG, "an operand's pointers are NULL or its strides too small");
+    if ((reinterpret_cast<uintptr_t>(o->q) & 15) || (o->rows > 1 && o->ld % 16))
+      return block_fail(MUONH_ERR_ALIGNMENT, "operands need 16-byte aligned rows");
+  }
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (k == 0) {
+    if (accumulate) return MUONH_OK;
+    clear_rows_kernel<<<dim3(static_cast<unsigned>(std::min<int64_t>((b->rows * size + 255) / 256, 64)),
+                             static_cast<unsigned>(std::min<int64_t>(a->rows, 4096))),
+                        256, 0, s>>>(static_cast<uint8_t*>(d), ldd * size, b->rows * size, a->rows);
+    return cudaGetLastError() == cudaSuccess ? MUONH_OK : block_fail(MUONH_ERR_CUDA, "launch of clear_rows_kernel failed");
+  }
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  BlockParams p{};
+  p.sa = a->scale;
+  p.sb = b->scale;
+  p.ld_sa = a->ld_scale;
+  p.ld_sb = b->ld_scale;
+  p.sa_shift = a->block_rows == 128 ? 7 : 0;
+  p.sb_shift = b->block_rows == 128 ? 7 : 0;
+  auto words = [](const muonh_block_operand* o) {
+    return (reinterpret_cast<uintptr_t>(o->scale) & 3) == 0 && (o->rows <= o->block_rows || o->ld_scale % 4 == 0);
+  };
+  p.sa_words = words(a);
+  p.sb_words = words(b);
+  p.d = d;
+  p.ldd = ldd;
+  p.m = static_cast<int32_t>(a->rows);
+  p.n = static_cast<int32_t>(b->rows);
+  p.k_blocks = static_cast<int32_t>(k_blocks);
+  p.dtype = dtype;
+  p.accumulate = accumulate != 0;
+  p.wide_store = (reinterpret_cast<uintptr_t>(d) & 31) == 0 && (a->rows == 1 || ldd * size % 32 == 0);
+  p.tiles_m = (p.m + kTm - 1) / kTm;
+  // narrower tiles where 256 columns would leave most SMs without one
+  auto tiles = [&](int bn) { return static_cast<int64_t>(p.tiles_m) * ((p.n + bn - 1) / bn); };
+  const int bn = tiles(256) >= sms ? 256 : tiles(128) >= sms ? 128 : 64;
+  p.tiles_n = (p.n + bn - 1) / bn;
+  p.band = 16;
+  CUtensorMap amap, bmap;
+  auto map = [&](CUtensorMap* out, const muonh_block_operand* o, int box_rows) {
+    return encode_bytes(out, const_cast<void*>(o->q), k, o->rows, o->rows == 1 ? (k + 15) / 16 * 16 : o->ld, box_rows);
+  };
+  if (!map(&amap, a, kTm) || !map(&bmap, b, bn)) return block_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const int grid = static_cast<int>(std::min<int64_t>(tiles(bn), sms));
+  const cudaError_t e = bn == 256   ? launch_block<256>(p, amap, bmap, grid, s)
+                        : bn == 128 ? launch_block<128>(p, amap, bmap, grid, s)
+                                    : launch_block<64>(p, amap, bmap, grid, s);
+  if (e != cudaSuccess) return block_fail(MUONH_ERR_CUDA, "launch of block_matmul_kernel failed");
+  return MUONH_OK;
+}
+
+cudaError_t muonh::take_block_timeout(int* flag, cudaStream_t s) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_block_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *flag)
+    e = cudaMemcpyToSymbolAsync(g_block_timeout, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e;
+}

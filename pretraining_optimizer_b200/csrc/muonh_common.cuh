@@ -450,8 +450,13 @@ void ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t*
 bool encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t cols, int64_t rows, int64_t batch,
                         int64_t ld, int64_t stride, int box_rows);
 
+// 2-D map over a matrix of bytes (rows x cols, row stride ld) with boxes of
+// 128 columns and box_rows rows (128-byte swizzle).
+bool encode_bytes(CUtensorMap* out, void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+
 // Reads and clears the record that a bounded wait gave up; synchronises s.
 cudaError_t take_orth_timeout(int* flag, cudaStream_t s);
+cudaError_t take_block_timeout(int* flag, cudaStream_t s);
 
 // Message returned by muonh_last_error() on the calling thread.
 void set_error_message(const char* msg);

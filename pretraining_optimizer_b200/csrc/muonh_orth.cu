@@ -125,14 +125,74 @@ __device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r,
   }
 }
 
-// 16 bytes of another CTA's shared memory.
+// 16 bytes of another CTA's shared memory (the callers' cluster barriers order it).
 __device__ __forceinline__ float4 load_cluster(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
+}
+
+// The sum over the cluster's R CTAs of the 64 values of each epilogue thread,
+// which every CTA has left at smem as 16 vectors per thread.  Each CTA adds
+// 16/R of the vectors, in rank order, and then all fetch each other's: 2 x 64
+// KB per CTA instead of R x 64 KB, and the same sums everywhere.  Loads start
+// at the next CTA, so that no CTA's shared memory is read by all at once.
+// All threads call it, between two cluster barriers.
+template <int R>
+__device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (&acc)[64]) {
+  constexpr int kEach = 16 / R;
+  const bool mine = threadIdx.x >= 64;
+  const uint32_t at = (threadIdx.x - 64) * 16;
+  float4* const own = reinterpret_cast<float4*>(smem) + (threadIdx.x - 64);
+  if (mine) {
+    float4 v[16];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t from = map_shared_rank(smem, (rank + 1 + i) % R) + at;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) v[i * kEach + j] = load_cluster(from + (rank * kEach + j) * kEpiThreads * 16);
+    }
+    // v[i] came from CTA (rank + 1 + i) % R: rotated back, so that the sum is in rank order
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (uint32_t r = 0; r < R; ++r) {
+        float4 w = v[j];
+#pragma unroll
+        for (int i = 1; i < R; ++i)
+          if ((rank + 1 + i) % R == r) w = v[i * kEach + j];
+        sum.x += w.x;
+        sum.y += w.y;
+        sum.z += w.z;
+        sum.w += w.w;
+      }
+      own[(rank * kEach + j) * kEpiThreads] = sum;
+    }
+  }
+  cluster_sync();
+  if (mine) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t r = (rank + 1 + i) % R;
+      const uint32_t from = map_shared_rank(smem, r) + at;
+      // the vectors of CTA r are numbers r kEach and on; acc is indexed statically
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const float4 v = load_cluster(from + (r * kEach + j) * kEpiThreads * 16);
+#pragma unroll
+        for (int s = 0; s < R; ++s)
+          if (static_cast<uint32_t>(s) == r) {
+            acc[4 * (s * kEach + j)] = v.x;
+            acc[4 * (s * kEach + j) + 1] = v.y;
+            acc[4 * (s * kEach + j) + 2] = v.z;
+            acc[4 * (s * kEach + j) + 3] = v.w;
+          }
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -276,21 +336,12 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   }
   if (ranks > 1) {
     cluster_sync();
-    if (warp >= 2) {
-#pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0.f;
-      for (uint32_t r = 0; r < ranks; ++r) {
-        const uint32_t theirs = map_shared_rank(smem, r) + (threadIdx.x - 64) * 16;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float4 v = load_cluster(theirs + j * kEpiThreads * 16);
-          acc[4 * j] += v.x;
-          acc[4 * j + 1] += v.y;
-          acc[4 * j + 2] += v.z;
-          acc[4 * j + 3] += v.w;
-        }
-      }
-    }
+    if (ranks == 2)
+      add_shares<2>(smem, rank, acc);
+    else if (ranks == 4)
+      add_shares<4>(smem, rank, acc);
+    else
+      add_shares<8>(smem, rank, acc);
     cluster_sync();
   }
 

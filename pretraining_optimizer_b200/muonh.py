@@ -28,6 +28,7 @@ EXPORTED_SYMBOLS = (
     "muonh_average",
     "muonh_adamw_step", "muonh_layer_norm", "muonh_layer_norm_workspace", "muonh_layer_norm_backward",
     "muonh_orthogonalize", "muonh_orthogonalize_workspace", "muonh_operator_status",
+    "muonh_block_quantize", "muonh_block_matmul",
     "muonh_check_wait_timeout", "muonh_destroy", "muonh_status_string", "muonh_last_error",
 )
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
@@ -68,6 +69,11 @@ class OrthogonalizeDesc(Structure):
                 ("x_stride", c_int64), ("ldx", c_int64), ("out_stride", c_int64), ("ldo", c_int64),
                 ("dtype", c_int32), ("ns_steps", c_int32), ("ns_a", c_float), ("ns_b", c_float),
                 ("ns_c", c_float), ("eps", c_float)]
+
+
+class BlockOperand(Structure):
+    _fields_ = [("q", c_void_p), ("scale", c_void_p), ("rows", c_int64), ("ld", c_int64), ("ld_scale", c_int64),
+                ("block_rows", c_int32), ("pad_", c_int32)]
 
 
 class MuonHError(RuntimeError):
@@ -120,6 +126,10 @@ def library() -> ctypes.CDLL:
     lib.muonh_orthogonalize.argtypes = [POINTER(OrthogonalizeDesc), c_void_p, c_size_t, c_void_p]
     lib.muonh_orthogonalize_workspace.argtypes = [POINTER(OrthogonalizeDesc)]
     lib.muonh_orthogonalize_workspace.restype = c_size_t
+    lib.muonh_block_quantize.argtypes = [c_void_p, c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p, c_int64,
+                                         c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+    lib.muonh_block_matmul.argtypes = [POINTER(BlockOperand), POINTER(BlockOperand), c_int64, c_void_p, c_int64,
+                                       c_int32, c_int32, c_void_p]
     lib.muonh_operator_status.argtypes = [c_void_p]
     lib.muonh_check_wait_timeout.argtypes = [ctypes.c_double, c_void_p]
     lib.muonh_destroy.argtypes = [c_void_p]
@@ -132,7 +142,8 @@ def library() -> ctypes.CDLL:
                  "muonh_export_state", "muonh_import_state", "muonh_device_status",
                  "muonh_enable_timing", "muonh_phase_times", "muonh_phase_flops", "muonh_momentum_norm_noalloc",
                  "muonh_average", "muonh_adamw_step", "muonh_check_wait_timeout", "muonh_layer_norm",
-                 "muonh_layer_norm_backward", "muonh_orthogonalize", "muonh_operator_status"):
+                 "muonh_layer_norm_backward", "muonh_orthogonalize", "muonh_operator_status",
+                 "muonh_block_quantize", "muonh_block_matmul"):
         getattr(lib, name).restype = c_int32
     _LIB = lib
     return lib

@@ -1,5 +1,5 @@
-"""ctypes bindings of the operators around the update: layer norm, and
-orthogonalising stacks of matrices.
+"""ctypes bindings of the operators around the update: layer norm, 8-bit
+products with block scales, and orthogonalising stacks of matrices.
 
 Like the rest of the binding these calls check and marshal arguments; the work
 is in the library's CUDA kernels.  Each call runs on the device of its tensors,
@@ -11,7 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, OrthogonalizeDesc, _check, library
+from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, BlockOperand, OrthogonalizeDesc, _check, library
 
 
 def _dtype_code(dtype):
@@ -180,6 +180,98 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
         size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))
         work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
         _check(lib.muonh_orthogonalize(ctypes.byref(d), None if work is None else work.data_ptr(), size, handle))
+    return out
+
+
+def _matrix(t, what: str):
+    """(pointer, rows, cols, row stride) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what} must have rows that do not overlap")
+    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+
+
+def _quantize(x, block_rows, rows, columns, stream):
+    import torch
+    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    xp, m, n, ldx = _matrix(x, "x")
+    out = []
+
+    def room(r, c):
+        """r x c bytes with a row stride that is a multiple of 16, and their scales."""
+        ld, groups = -(-c // 16) * 16, -(-c // 128)
+        q = torch.empty((r, ld), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((-(-r // block_rows), groups), dtype=torch.uint8, device=x.device)
+        out.extend((q if ld == c else q[:, :c], s))
+        return q.data_ptr(), ld, s.data_ptr(), groups
+
+    with _on(x.device, stream) as handle:
+        args = room(m, n) if rows else (None, 0, None, 0)
+        args += room(n, m) if columns else (None, 0, None, 0)
+        _check(library().muonh_block_quantize(xp, ldx, m, n, _dtype_code(x.dtype), block_rows, *args, handle))
+    return tuple(out)
+
+
+def block_quantize(x, rows=True, columns=False, stream=None):
+    """x [m, n] (fp32, bf16 or fp16) in e4m3 with a power-of-two scale for each
+    1 x 128 group: (q, scale) along its rows, and with columns=True also (qt,
+    scale_t), its transpose in groups along x's columns (the weight gradient's
+    operand).  q is float8_e4m3fn with a row stride that is a multiple of 16,
+    scale is uint8 [m, ceil(n / 128)], the exponent plus 127."""
+    if not rows and not columns:
+        raise ValueError("rows or columns must be true")
+    return _quantize(x, 1, rows, columns, stream)
+
+
+def block_quantize_weight(w, stream=None):
+    """w [n, k] in e4m3 with a scale for each 128 x 128 block, and its transpose:
+    (q, scale, qt, scale_t), for the forward product and the activation gradient."""
+    return _quantize(w, 128, True, True, stream)
+
+
+def _block_operand(q, scale, what: str, device):
+    import torch
+    _tensor(q, what, (torch.float8_e4m3fn,), device)
+    _tensor(scale, f"{what}_scale", (torch.uint8,), device)
+    qp, rows, k, ld = _matrix(q, what)
+    sp, srows, groups, lds = _matrix(scale, f"{what}_scale")
+    if groups != -(-k // 128) or srows not in (rows, -(-rows // 128)):
+        raise ValueError(f"{what}_scale must be [{rows} or {-(-rows // 128)}, {-(-k // 128)}] for {what} [{rows}, {k}]")
+    return BlockOperand(qp, sp, rows, ld, lds, 1 if srows == rows else 128, 0), rows, k
+
+
+def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=False, stream=None):
+    """a b^T for operands of block_quantize or block_quantize_weight: a [m, k]
+    and b [n, k] in float8_e4m3fn with uint8 scales for each row or each 128
+    rows, and each 128 columns.  Returns [m, n] in dtype (bf16 by default; fp32
+    or fp16) or writes to `out`; accumulate=True adds to an fp32 `out`, such as
+    the gradient that MuonH.step reads."""
+    import torch
+    ao, m, k = _block_operand(a, a_scale, "a", None)
+    bo, n, kb = _block_operand(b, b_scale, "b", a.device)
+    _tensor(a_scale, "a_scale", (torch.uint8,), a.device)
+    if k != kb:
+        raise ValueError("a and b must have the same number of columns")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        dtype = torch.bfloat16 if dtype is None else dtype
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError("out must be of dtype")
+    with _on(a.device, stream) as handle:
+        if out is None:
+            if _dtype_code(dtype) is None:
+                raise TypeError("dtype must be torch.float32, torch.bfloat16 or torch.float16")
+            out = torch.empty((m, n), dtype=dtype, device=a.device)
+        _tensor(out, "out", (torch.float32, torch.bfloat16, torch.float16), a.device)
+        if out.shape != (m, n):
+            raise ValueError(f"out must be [{m}, {n}]")
+        op, _, _, ldo = _matrix(out, "out")
+        _check(library().muonh_block_matmul(ctypes.byref(ao), ctypes.byref(bo), k, op, ldo, _dtype_code(out.dtype),
+                                            int(bool(accumulate)), handle))
     return out
 
 

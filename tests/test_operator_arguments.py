@@ -134,3 +134,57 @@ def test_orthogonalize_binding_rejects():
     for bad in (x.mT, x[:, :, ::2], x[:, :1].expand(3, 6, 10)):
         with pytest.raises(ValueError):
             _stack(bad, "x")
+
+
+def test_block_quantize_checks():
+    f = P.library().muonh_block_quantize
+    ok = dict(x=A, ldx=64, rows=4, cols=64, dtype=1, block_rows=1, q=A, ldq=64, s=A, lds=1, qt=A, ldqt=16, st=A,
+              ldst=1, stream=None)
+
+    def call(**kw):
+        return f(*{**ok, **kw}.values())
+
+    assert call(rows=-1) == 1 and call(cols=-1) == 1 and call(rows=2 ** 24) == 1 and call(cols=2 ** 31) == 1
+    assert call(dtype=3) == 1 and call(block_rows=64) == 1
+    assert call(x=None) == 1 and call(q=None, qt=None) == 1 and call(s=None) == 1 and call(st=None) == 1
+    assert call(ldx=63) == 1 and call(ldq=48) == 1 and call(ldqt=0) == 1 and call(lds=0) == 1 and call(ldst=0) == 1
+    assert call(cols=200, ldx=200, ldq=208, lds=1) == 1
+    assert call(x=A + 1) == 2 and call(q=A + 8) == 2 and call(ldq=72) == 2 and call(qt=A + 4) == 2 and call(ldqt=20) == 2
+    assert call(rows=0, x=None, q=None, qt=None) == 0 and call(cols=0) == 0
+
+
+def test_block_matmul_checks():
+    from pretraining_optimizer_b200.muonh import BlockOperand as Op
+    f = P.library().muonh_block_matmul
+    assert ctypes.sizeof(Op) == 48 and Op.ld.offset == 24 and Op.block_rows.offset == 40
+
+    def call(a=None, b=None, k=300, d=A, ldd=64, dtype=1, accumulate=0):
+        ok = dict(q=A, scale=A, rows=32, ld=304, ld_scale=3, block_rows=1, pad_=0)
+        x = Op(*{**ok, **(a or {})}.values())
+        y = Op(*{**ok, "rows": 64, **(b or {})}.values())
+        return f(ctypes.byref(x), ctypes.byref(y), k, d, ldd, dtype, accumulate, None)
+
+    x = Op()
+    assert f(None, ctypes.byref(x), 1, A, 1, 0, 0, None) == 1 and f(ctypes.byref(x), None, 1, A, 1, 0, 0, None) == 1
+    for side in ("a", "b"):
+        assert call(**{side: dict(rows=-1)}) == 1 and call(**{side: dict(block_rows=2)}) == 1
+        assert call(**{side: dict(q=None)}) == 1 and call(**{side: dict(scale=None)}) == 1
+        assert call(**{side: dict(ld=288)}) == 1 and call(**{side: dict(ld_scale=2)}) == 1
+        assert call(**{side: dict(q=A + 4)}) == 2 and call(**{side: dict(ld=301)}) == 2
+        assert call(**{side: dict(rows=0, q=None)}) == 0
+    assert call(k=-1) == 1 and call(dtype=4) == 1 and call(dtype=1, accumulate=1) == 1
+    assert call(d=None) == 1 and call(ldd=63) == 1 and call(d=A + 1) == 2 and call(dtype=0, d=A + 2) == 2
+    assert call(k=0, dtype=0, accumulate=1) == 0
+
+
+def test_block_binding_rejects():
+    import torch
+    x = torch.zeros(4, 128)
+    with pytest.raises(TypeError):
+        P.block_quantize(x)
+    with pytest.raises(TypeError):
+        P.block_quantize_weight(x)
+    with pytest.raises(ValueError):
+        P.block_quantize(x, rows=False)
+    with pytest.raises(TypeError):
+        P.block_matmul(x, x, x, x)
