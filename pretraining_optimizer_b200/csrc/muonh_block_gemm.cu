@@ -9,16 +9,23 @@
 // four MMAs that use the same scale byte.  A 32-bit TMEM word per row holds the
 // bytes of four k-blocks (512 of k); the instruction descriptor picks the byte.
 //
-// One persistent CTA per SM computes 128 x BN tiles (BN = 256 where there are
-// enough tiles).  Warp 0 loads operands by TMA (one k-block of 128 bytes is one
-// 128-byte swizzled row), warp 2 gathers the scale words of both operands into
-// shared memory, warp 1 copies them to TMEM (tcgen05.cp) and issues the MMAs,
-// and warps 4 to 11 drain the accumulator, round once and store.
+// Two shapes of the same kernel, persistent with one CTA per SM:
+//   pair    a cluster of two CTAs computes 256 x 256 tiles with cta_group::2, each
+//           CTA loading its 128 rows of A and half of the 256 rows of B.  A CTA
+//           then fetches 32 KB per 128 of k for 128 x 256 results, against 48 KB
+//           for a 128 x 256 tile of its own: L2 bandwidth is what bounds that one.
+//   single  128 x 128 or 128 x 64 tiles, where the pair's would leave SMs idle.
+// Warps 0 and 3 load A and B by TMA (one k-block of 128 bytes is one 128-byte
+// swizzled row; a TMA instruction holds its thread for hundreds of cycles, so one
+// warp for both could not keep up), warp 2 gathers the scale words of both operands into shared memory, warp
+// 1 copies them to TMEM (tcgen05.cp) and issues the MMAs, and warps 4 to 11 take
+// the accumulator into registers, hand it back, round once and store.
 //
 // The tensor cores' fp32 accumulation truncates, with an error that grows with
-// the number of products added up.  fp32 results are therefore accumulated
-// over at most kChunkBlocks k-blocks in TMEM, and the chunks are added in IEEE
-// fp32 in the result itself, by the thread that wrote it.
+// the number of products added up (5e-7 of the result's norm at k = 8192, for
+// random operands).  fp32 results are therefore accumulated over at most
+// kChunkBlocks k-blocks in TMEM, and the chunks are added in IEEE fp32 in the
+// result itself, by the thread that wrote it: 8e-8.
 #include <algorithm>
 
 #include "muonh_common.cuh"
@@ -31,14 +38,18 @@ constexpr int kKBlock = 128;                     // k per stage: one scale block
 constexpr int kThreads = 384;
 constexpr int kEpi = 256;                        // epilogue threads
 constexpr int kScaleRing = 4;                    // scale words in flight: 512 of k each
-constexpr int kChunkBlocks = 8;                  // fp32 results: k-blocks per TMEM accumulation
+constexpr int kChunkBlocks = 16;                 // fp32 results: k-blocks per TMEM accumulation
 
-template <int BN>
+// PAIR: BN is 256, shared by the two CTAs.
+template <int BN, bool PAIR>
 struct BlockCfg {
+  static_assert(!PAIR || BN == 256, "a pair computes 256 x 256 tiles");
+  static constexpr int kTileRows = PAIR ? 2 * kTm : kTm;
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;    // rows of B that this CTA loads
   static constexpr int kABytes = kTm * kKBlock;
-  static constexpr int kBBytes = BN * kKBlock;
+  static constexpr int kBBytes = kBRows * kKBlock;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kStages = 6;
   static constexpr int kAccs = BN == 256 ? 1 : 2;      // accumulators in TMEM, next to the scales
   static constexpr int kScaleBlocks = 1 + (BN + 127) / 128;   // 512-byte blocks of scale words: A, and B per 128 rows
   static constexpr int kScaleBytes = kScaleBlocks * 512;
@@ -75,9 +86,33 @@ __device__ __forceinline__ void umma_mxf8(uint32_t d, uint64_t adesc, uint64_t b
       : "memory");
 }
 
+// The same over a CTA pair: 256 rows of A, half in each CTA.
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
+                                               uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
 // 32 rows of 16 bytes from shared memory to 4 TMEM columns of lanes 0..31, repeated for the other three lane groups.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// ... in both CTAs of a pair, each from its own shared memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
 }
 
 // Descriptor of that 512-byte block: no swizzle, 8 rows of 16 bytes per 128 bytes.
@@ -127,7 +162,7 @@ __device__ __forceinline__ void store32(void* p, const Vec32& v) {
 }
 
 // 32 results of one row.  `add`: fp32 results are added to what is there.
-__device__ __forceinline__ void store_row(const BlockParams& p, int row, int col, float (&v)[32], bool add) {
+__device__ __forceinline__ void store_row(const BlockParams& p, int row, int col, float* v, bool add) {
   if (row >= p.m || col >= p.n) return;
   if (p.dtype == MUONH_DTYPE_F32) {
     float* d = static_cast<float*>(p.d) + static_cast<int64_t>(row) * p.ldd + col;
@@ -179,11 +214,12 @@ __device__ __forceinline__ void store_row(const BlockParams& p, int row, int col
   }
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     block_matmul_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap amap,
                         const __grid_constant__ CUtensorMap bmap) {
-  using C = BlockCfg<BN>;
+  using C = BlockCfg<BN, PAIR>;
+  constexpr int kCtas = PAIR ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
@@ -196,6 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;   // 0 = leader: issues the MMAs, holds full, sfull and tempty
+  const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -203,104 +241,156 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) {
-      mbar_init(&sfull[s], 32);
+      mbar_init(&sfull[s], 32 * kCtas);
       mbar_init(&sempty[s], 1);
     }
     for (int a = 0; a < C::kAccs; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kEpi);
+      mbar_init(&tempty[a], kEpi * kCtas);
     }
     mbar_init(drain, 1);
     *err = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  if (warp == 1) {
+    if (PAIR)
+      tmem_alloc_pair(tmem_slot, 512);
+    else
+      tmem_alloc(tmem_slot, 512);
+  }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                      // barriers initialised in both CTAs
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  auto arrive_leader = [&](uint64_t* bar) {
+    if (PAIR)
+      mbar_arrive_cluster(map_shared_rank(bar, 0));
+    else
+      mbar_arrive(bar);
+  };
+  auto commit = [&](uint64_t* bar) {             // in both CTAs of a pair
+    if (PAIR)
+      umma_commit_pair(bar);
+    else
+      umma_commit(bar);
+  };
 
   // every role walks over the same (tile, chunk of k) sequence
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int chunk = p.dtype == MUONH_DTYPE_F32 ? kChunkBlocks : p.k_blocks;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
-      // ---------------------------------------------------------- TMA producer
-      int64_t i = 0;                             // k-blocks issued
+      // ---------------------------------------------------------- TMA producers
+      const bool role_a = warp == 0;             // also announces the stage's bytes
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;                            // up to kStages
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int64_t t = worker; t < tiles && ok; t += workers) {
         int tm, tn;
         tile_at(p, t, tm, tn);
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++i) {
-          const int s = static_cast<int>(i % C::kStages);
-          if (i >= C::kStages && !mbar_wait(&empty[s], static_cast<uint32_t>(i / C::kStages - 1) & 1, err)) {
+        const int row = role_a ? tm * C::kTileRows + static_cast<int>(rank) * kTm
+                               : tn * BN + static_cast<int>(rank) * C::kBRows;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, err)) {
             ok = false;
             break;
           }
-          mbar_expect_tx(&full[s], C::kStageBytes);
-          uint8_t* dst = smem + s * C::kStageBytes;
-          tma_load_2d(dst, &amap, &full[s], kb * kKBlock, tm * kTm);
-          tma_load_2d(dst + C::kABytes, &bmap, &full[s], kb * kKBlock, tn * BN);
+          if (rank == 0 && role_a) mbar_expect_tx(&full[stage], kCtas * C::kStageBytes);
+          uint8_t* dst = smem + stage * C::kStageBytes + (role_a ? 0 : C::kABytes);
+          if (PAIR)
+            tma_load_2d_pair(dst, role_a ? &amap : &bmap, map_shared_rank(&full[stage], 0), kb * kKBlock, row);
+          else
+            tma_load_2d(dst, role_a ? &amap : &bmap, &full[stage], kb * kKBlock, row);
+          if (issued < C::kStages) ++issued;
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
-      // copies in flight land before the CTA may exit
-      for (int64_t j = std::max<int64_t>(0, i - C::kStages); j < i; ++j) {
+      // copies in flight land before a CTA may exit
+      for (int j = 0; j < issued && rank == 0; ++j) {
+        if (--stage < 0) {
+          stage = C::kStages - 1;
+          phase ^= 1u;
+        }
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(&full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1) &&
-               globaltimer() - t0 < kWaitLimitNs) {
+        while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitLimitNs) {
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer
-      int64_t i = 0, g = 0, work = 0;            // k-blocks, scale words and accumulators used
+      int stage = 0, ring = 0, acc = 0;
+      uint32_t phase = 0, ring_phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < p.k_blocks && ok; ++kb, ++i) {
-          const int acc = static_cast<int>(work % C::kAccs);
-          if (kb % chunk == 0) {
-            if (work >= C::kAccs && !mbar_wait(&tempty[acc], static_cast<uint32_t>(work / C::kAccs - 1) & 1, err)) {
+      for (int64_t t = worker; t < tiles && ok; t += workers) {
+        int left = 0;                            // k-blocks until the accumulator is complete
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          const bool fresh = left == 0;
+          if (fresh) {
+            left = min(chunk, p.k_blocks - kb);
+            if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, err)) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          const int ring = static_cast<int>(g % kScaleRing);
           const uint32_t sc = tmem + C::kScaleCol + ring * 16;
           if ((kb & 3) == 0) {
             // copies and MMAs of one thread run in the order that they are
             // issued in, so the words are in place for the MMAs below and the
             // ones that they replace have been used
-            if (!mbar_wait(&sfull[ring], static_cast<uint32_t>(g / kScaleRing) & 1, err)) {
+            if (!mbar_wait(&sfull[ring], ring_phase, err)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t from = smem_u32(smem + C::kScaleOffset + ring * C::kScaleBytes);
 #pragma unroll
-            for (int b = 0; b < C::kScaleBlocks; ++b) copy_scales(sc + 4 * b, scale_desc(from + 512 * b));
-            umma_commit(&sempty[ring]);
+            for (int b = 0; b < C::kScaleBlocks; ++b) {
+              if (PAIR)
+                copy_scales_pair(sc + 4 * b, scale_desc(from + 512 * b));
+              else
+                copy_scales(sc + 4 * b, scale_desc(from + 512 * b));
+            }
+            commit(&sempty[ring]);
           }
-          const int s = static_cast<int>(i % C::kStages);
-          if (!mbar_wait(&full[s], static_cast<uint32_t>(i / C::kStages) & 1, err)) {
+          if (!mbar_wait(&full[stage], phase, err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
-          const uint32_t idesc = idesc_mxf8(kTm, BN, kb & 3);
+          const uint32_t a = smem_u32(smem + stage * C::kStageBytes), b = a + C::kABytes;
+          const uint32_t idesc = idesc_mxf8(C::kTileRows, BN, kb & 3);
 #pragma unroll
-          for (int k = 0; k < kKBlock / 32; ++k)
-            umma_mxf8(tmem + acc * 128, sdesc_sw128(a + k * 32, 16, 1024), sdesc_sw128(b + k * 32, 16, 1024), idesc,
-                      sc, sc + 4, (kb % chunk) != 0 || k != 0);
-          umma_commit(&empty[s]);
-          if ((kb & 3) == 3 || kb == p.k_blocks - 1) ++g;
-          if (kb % chunk == chunk - 1 || kb == p.k_blocks - 1) {
-            umma_commit(&tfull[acc]);
-            ++work;
+          for (int k = 0; k < kKBlock / 32; ++k) {
+            const uint64_t ad = sdesc_sw128(a + k * 32, 16, 1024), bd = sdesc_sw128(b + k * 32, 16, 1024);
+            if (PAIR)
+              umma_mxf8_pair(tmem + acc * 128, ad, bd, idesc, sc, sc + 4, !fresh || k != 0);
+            else
+              umma_mxf8(tmem + acc * 128, ad, bd, idesc, sc, sc + 4, !fresh || k != 0);
+          }
+          commit(&empty[stage]);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (((kb & 3) == 3 || kb == p.k_blocks - 1) && ++ring == kScaleRing) {
+            ring = 0;
+            ring_phase ^= 1u;
+          }
+          if (--left == 0) {
+            commit(&tfull[acc]);
+            if (++acc == C::kAccs) {
+              acc = 0;
+              acc_phase ^= 1u;
+            }
           }
         }
       }
@@ -313,18 +403,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 2) {
     // --------------------------------------------------------- scale words
-    // row r of a block of 128 is word r / 32 of the 16 bytes of TMEM lane r % 32
-    int64_t g = 0;
+    // row r of a block of 128 is word r / 32 of the 16 bytes of TMEM lane r % 32;
+    // a pair's CTAs each need the words of their own rows of A and of all of B
+    int ring = 0;
+    uint32_t ring_phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int64_t t = worker; t < tiles && ok; t += workers) {
       int tm, tn;
       tile_at(p, t, tm, tn);
-      for (int w = 0; 4 * w < p.k_blocks && ok; ++w, ++g) {
-        const int ring = static_cast<int>(g % kScaleRing);
+      const int arow = tm * C::kTileRows + static_cast<int>(rank) * kTm;
+      for (int w = 0; 4 * w < p.k_blocks; ++w) {
         uint32_t u[C::kScaleBlocks][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          u[0][j] = scale_word(p.sa, p.ld_sa, p.sa_shift, p.sa_words, tm * kTm + 32 * j + lane, p.m, w, p.k_blocks);
+          u[0][j] = scale_word(p.sa, p.ld_sa, p.sa_shift, p.sa_words, arow + 32 * j + lane, p.m, w, p.k_blocks);
 #pragma unroll
         for (int b = 1; b < C::kScaleBlocks; ++b)
 #pragma unroll
@@ -333,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           ? scale_word(p.sb, p.ld_sb, p.sb_shift, p.sb_words, tn * BN + 128 * (b - 1) + 32 * j + lane,
                                        p.n, w, p.k_blocks)
                           : 0x7f7f7f7fu;
-        if (g >= kScaleRing && !mbar_wait(&sempty[ring], static_cast<uint32_t>(g / kScaleRing - 1) & 1, err)) ok = false;
+        if (!mbar_wait(&sempty[ring], ring_phase ^ 1u, err)) ok = false;
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -343,7 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < C::kScaleBlocks; ++b)
           *reinterpret_cast<uint4*>(to + 512 * b) = make_uint4(u[b][0], u[b][1], u[b][2], u[b][3]);
         fence_proxy_async_smem();
-        mbar_arrive(&sfull[ring]);
+        arrive_leader(&sfull[ring]);
+        if (++ring == kScaleRing) {
+          ring = 0;
+          ring_phase ^= 1u;
+        }
       }
     }
   } else if (warp >= 4) {
@@ -351,38 +447,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = BN / 2;                // columns per thread
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    int64_t work = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int64_t t = worker; t < tiles && ok; t += workers) {
       int tm, tn;
       tile_at(p, t, tm, tn);
-      const int row = tm * kTm + quarter * 32 + lane, col = tn * BN + half * kCols;
-      for (int kb = 0; kb < p.k_blocks; kb += chunk, ++work) {
-        const int acc = static_cast<int>(work % C::kAccs);
-        if (!mbar_wait(&tfull[acc], static_cast<uint32_t>(work / C::kAccs) & 1, err)) {
+      const int row = tm * C::kTileRows + static_cast<int>(rank) * kTm + quarter * 32 + lane;
+      const int col = tn * BN + half * kCols;
+      for (int kb = 0; kb < p.k_blocks; kb += chunk) {
+        if (!mbar_wait(&tfull[acc], acc_phase, err)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // all of it into registers first: the next tile's MMAs wait for this
+        float v[kCols / 32][32];
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tmem + lanes + acc * 128 + half * kCols + 32 * c, v[c]);
+        tc_fence_before();
+        arrive_leader(&tempty[acc]);
+        if (++acc == C::kAccs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
         const bool add = kb > 0 || p.accumulate;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          float v[32];
-          tmem_ld32(tmem + lanes + acc * 128 + half * kCols + c, v);
-          if (c + 32 == kCols) {
-            tc_fence_before();
-            mbar_arrive(&tempty[acc]);
-          }
-          store_row(p, row, col + c, v, add);
-        }
+        for (int c = 0; c < kCols / 32; ++c) store_row(p, row, col + 32 * c, v[c], add);
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();                      // neither CTA's memory is in use by the other
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
   if (threadIdx.x == 0 && *err) atomicOr(&g_block_timeout, 1);
 }
 
@@ -398,13 +503,24 @@ muonh_status block_fail(muonh_status st, const char* msg) {
   return st;
 }
 
-template <int BN>
-cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(block_matmul_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             BlockCfg<BN>::kSmem);
+template <int BN, bool PAIR>
+cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUtensorMap& b, int workers, cudaStream_t s) {
+  const auto kernel = block_matmul_kernel<BN, PAIR>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockCfg<BN, PAIR>::kSmem);
   if (e != cudaSuccess) return e;
-  block_matmul_kernel<BN><<<grid, kThreads, BlockCfg<BN>::kSmem, s>>>(p, a, b);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * workers : workers));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = BlockCfg<BN, PAIR>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = PAIR ? 2 : 1;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, a, b);
 }
 
 }  // namespace
@@ -468,21 +584,25 @@ extern "C" muonh_status muonh_block_matmul(const muonh_block_operand* a, const m
   p.dtype = dtype;
   p.accumulate = accumulate != 0;
   p.wide_store = (reinterpret_cast<uintptr_t>(d) & 31) == 0 && (a->rows == 1 || ldd * size % 32 == 0);
-  p.tiles_m = (p.m + kTm - 1) / kTm;
-  // narrower tiles where 256 columns would leave most SMs without one
-  auto tiles = [&](int bn) { return static_cast<int64_t>(p.tiles_m) * ((p.n + bn - 1) / bn); };
-  const int bn = tiles(256) >= sms ? 256 : tiles(128) >= sms ? 128 : 64;
+  // the pair's tiles where they fill the SMs, else narrower ones
+  auto tiles = [&](int rows, int cols) {
+    return static_cast<int64_t>((p.m + rows - 1) / rows) * ((p.n + cols - 1) / cols);
+  };
+  const bool pair = tiles(256, 256) >= sms / 2;
+  const int bn = pair ? 256 : tiles(128, 128) >= sms ? 128 : 64, rows = pair ? 256 : kTm;
+  p.tiles_m = (p.m + rows - 1) / rows;
   p.tiles_n = (p.n + bn - 1) / bn;
-  p.band = 16;
+  p.band = pair ? 8 : 16;
   CUtensorMap amap, bmap;
   auto map = [&](CUtensorMap* out, const muonh_block_operand* o, int box_rows) {
     return encode_bytes(out, const_cast<void*>(o->q), k, o->rows, o->rows == 1 ? (k + 15) / 16 * 16 : o->ld, box_rows);
   };
-  if (!map(&amap, a, kTm) || !map(&bmap, b, bn)) return block_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  const int grid = static_cast<int>(std::min<int64_t>(tiles(bn), sms));
-  const cudaError_t e = bn == 256   ? launch_block<256>(p, amap, bmap, grid, s)
-                        : bn == 128 ? launch_block<128>(p, amap, bmap, grid, s)
-                                    : launch_block<64>(p, amap, bmap, grid, s);
+  if (!map(&amap, a, kTm) || !map(&bmap, b, pair ? 128 : bn))
+    return block_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const int workers = static_cast<int>(std::min<int64_t>(tiles(rows, bn), pair ? sms / 2 : sms));
+  const cudaError_t e = pair        ? launch_block<256, true>(p, amap, bmap, workers, s)
+                        : bn == 128 ? launch_block<128, false>(p, amap, bmap, workers, s)
+                                    : launch_block<64, false>(p, amap, bmap, workers, s);
   if (e != cudaSuccess) return block_fail(MUONH_ERR_CUDA, "launch of block_matmul_kernel failed");
   return MUONH_OK;
 }

@@ -9,20 +9,25 @@
 // with a power of two is exact.  A block that holds NaN or Inf gets scale byte
 // 255 (NaN in E8M0) and NaN throughout.
 //
-// Bound by HBM: each element is read once and written once per orientation.  A
-// block of 256 threads takes a 128 x 128 tile, 8 x 8 elements per thread in
-// registers; maxima along rows come from 16 lanes' shuffles, maxima along
-// columns go through shared memory, and so does the transposed copy.
+// Bound by HBM: each element is read once and written once per orientation.
+// Rows alone need no tile: 16 lanes take a group of 128, four groups per thread
+// in flight.  For both orientations a block of 256 threads takes a 128 x 128
+// tile, 8 x 8 elements per thread in registers; maxima along rows come from 16
+// lanes' shuffles, maxima along columns go through shared memory, and so does
+// the transposed copy, its 8-byte pieces swizzled so that neither its writes
+// (down a column of pieces) nor its reads (along a row) meet in a bank.
 #include "muonh_common.cuh"
 
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 namespace muonh {
 namespace {
 
 constexpr int kTile = 128;
 constexpr int kQuantThreads = 256;
-constexpr int kTransposedPitch = kTile + 16;   // bytes per row of the transposed tile in shared memory
+constexpr int kRowsPerThread = 4;              // rows alone: groups in flight per thread
 
 struct QuantParams {
   const void* x;
@@ -35,9 +40,6 @@ struct QuantParams {
   int32_t whole;             // 1: one scale per 128 x 128 block
   int32_t vec;               // 16-byte loads of x
 };
-
-// |v| as ordered bits: NaN above Inf above every number.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Scale byte of a block whose largest magnitude has the bits m.
 // m = 1.f x 2^e <= 448 2^k = 1.75 x 2^(8 + k): k = e - 8, plus one where 1.f > 1.75.
@@ -57,14 +59,64 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
+// An 8-element piece of a row as it was loaded.
 template <typename T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+struct Piece {
+  static constexpr int kWords = 2 * sizeof(T);
+  uint32_t w[kWords];
+  // `vec`: p is 16-byte aligned and all 8 elements exist; else the first `left`, the others zero
+  __device__ __forceinline__ void load(const T* p, bool vec, int64_t left) {
+    if (vec) {
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[k];
+        w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+      }
+      return;
+    }
+    zero();
+    using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+    const Bits* b = reinterpret_cast<const Bits*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) {
+        if constexpr (sizeof(T) == 2)
+          w[j >> 1] |= static_cast<uint32_t>(b[j]) << (16 * (j & 1));
+        else
+          w[j] = b[j];
+      }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0u;
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    const uint32_t u = w[j >> 1];
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float((j & 1) ? (u & 0xffff0000u) : (u << 16));
+    const __half2 h = *reinterpret_cast<const __half2*>(&u);
+    return (j & 1) ? __high2float(h) : __low2float(h);
+  }
+};
+
+// Magnitudes in the type's own bits, ordered (NaN above Inf above numbers): one
+// 32-bit word per fp32 element, two 16-bit halves otherwise.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+  return w & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  return sizeof(T) == 4 ? max(a, b) : __vmaxs2(a, b);
+}
+// Those bits of one element as fp32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t as_f32_bits(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return m;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+}
 
 // 8 bytes of one output row; bytes behind the row's end are left as they were.
 __device__ __forceinline__ void store8(uint8_t* p, uint2 v, int64_t left) {
@@ -77,57 +129,96 @@ __device__ __forceinline__ void store8(uint8_t* p, uint2 v, int64_t left) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) block_quantize_kernel(const __grid_constant__ QuantParams p) {
-  __shared__ uint32_t column_max[kQuantThreads / 32][kTile];
-  __shared__ __align__(16) uint8_t turned[kTile * kTransposedPitch];
+__device__ __forceinline__ uint2 quantize_row(const Piece<T>& v, float f) {
+  return make_uint2(to_e4m3x4(v.at(0) * f, v.at(1) * f, v.at(2) * f, v.at(3) * f),
+                    to_e4m3x4(v.at(4) * f, v.at(5) * f, v.at(6) * f, v.at(7) * f));
+}
+
+// Groups of 128 along the rows alone; groups are numbered row by row.
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) block_quantize_rows_kernel(const __grid_constant__ QuantParams p) {
+  const uint32_t per_row = static_cast<uint32_t>((p.cols + kTile - 1) / kTile);
+  const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;   // below 2^31
+  const uint32_t first = blockIdx.x * (kRowsPerThread * kQuantThreads / 16) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  Piece<T> v[kRowsPerThread];
+  int64_t row[kRowsPerThread], col[kRowsPerThread];
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    const uint32_t u = first + i * (kQuantThreads / 16);
+    const uint32_t r = u / per_row;
+    row[i] = u < total ? r : p.rows;
+    col[i] = static_cast<int64_t>(u - r * per_row) * kTile + lane * 8;
+    if (row[i] < p.rows)
+      v[i].load(static_cast<const T*>(p.x) + row[i] * p.ldx + col[i], p.vec && col[i] < p.cols, p.cols - col[i]);
+    else
+      v[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerThread; ++i) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < Piece<T>::kWords; ++k) m = larger<T>(m, magnitudes<T>(v[i].w[k]));
+    if (sizeof(T) == 2) m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int b = scale_byte(as_f32_bits<T>(m));
+    if (row[i] >= p.rows) continue;
+    if (lane == 0) p.s[row[i] * p.lds + col[i] / kTile] = static_cast<uint8_t>(b);
+    if (col[i] < p.cols) store8(p.q + row[i] * p.ldq + col[i], quantize_row(v[i], inverse_scale(b)), p.cols - col[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t turned_piece(int row, int piece) {
+  return static_cast<uint32_t>(row * kTile + ((piece ^ ((row >> 3) & 15)) << 3));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
+    block_quantize_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int kWords = Piece<T>::kWords;
+  __shared__ uint32_t column_max[kQuantThreads / 32][kTile / 8 * kWords];
+  __shared__ __align__(16) uint8_t turned[kTile * kTile];
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile, c0 = static_cast<int64_t>(blockIdx.x) * kTile;
   const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;   // this thread's 8 columns and 8 rows
   const int64_t col = c0 + tc * 8;
 
-  float v[8][8];
+  Piece<T> v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + tr * 8 + i;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx + col;
-    if (row < p.rows && p.vec && col < p.cols) {            // vec: cols is a multiple of 8
-      uint4 u[sizeof(T) / 2];
-#pragma unroll
-      for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) u[k] = reinterpret_cast<const uint4*>(x)[k];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = as_float(reinterpret_cast<const T*>(u)[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = (row < p.rows && col + j < p.cols) ? as_float(x[j]) : 0.f;
-    }
+    if (row < p.rows)
+      v[i].load(static_cast<const T*>(p.x) + row * p.ldx + col, p.vec && col < p.cols, p.cols - col);
+    else
+      v[i].zero();
   }
 
-  uint32_t m_row[8], m_col[8];
+  uint32_t m_row[8], m_col[kWords];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m_row[i] = m_col[i] = 0u;
+  for (int k = 0; k < kWords; ++k) m_col[k] = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i) {
+    m_row[i] = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t m = magnitude(v[i][j]);
-      m_row[i] = max(m_row[i], m);
-      m_col[j] = max(m_col[j], m);
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t m = magnitudes<T>(v[i].w[k]);
+      m_row[i] = larger<T>(m_row[i], m);
+      m_col[k] = larger<T>(m_col[k], m);
     }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m_row[i] = max(m_row[i], __shfl_xor_sync(0xffffffffu, m_row[i], o));
+    if (sizeof(T) == 2) m_row[i] = max(m_row[i] & 0xffffu, m_row[i] >> 16);
+  }
 
   int b_row[8], b_col[8];
   if (p.whole) {
     uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, m_row[i]);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) column_max[threadIdx.x >> 5][0] = m;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, column_max[w][0]);
-    const int b = scale_byte(m);
+    const int b = scale_byte(as_f32_bits<T>(m));
 #pragma unroll
     for (int i = 0; i < 8; ++i) b_row[i] = b_col[i] = b;
     if (threadIdx.x == 0) {
@@ -138,26 +229,35 @@ __global__ void __launch_bounds__(kQuantThreads) block_quantize_kernel(const __g
     if (p.q) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        b_row[i] = scale_byte(m_row[i]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m_row[i] = max(m_row[i], __shfl_xor_sync(0xffffffffu, m_row[i], o));
+        b_row[i] = scale_byte(as_f32_bits<T>(m_row[i]));
         const int64_t row = r0 + tr * 8 + i;
         if (tc == 0 && row < p.rows) p.s[row * p.lds + blockIdx.x] = static_cast<uint8_t>(b_row[i]);
       }
     }
     if (p.qt) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t m = max(m_col[j], __shfl_xor_sync(0xffffffffu, m_col[j], 16));
-        if ((threadIdx.x & 16) == 0) column_max[threadIdx.x >> 5][tc * 8 + j] = m;
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t m = larger<T>(m_col[k], __shfl_xor_sync(0xffffffffu, m_col[k], 16));
+        if ((threadIdx.x & 16) == 0) column_max[threadIdx.x >> 5][tc * kWords + k] = m;
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int k = 0; k < kWords; ++k) {
         uint32_t m = 0u;
 #pragma unroll
-        for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, column_max[w][tc * 8 + j]);
-        b_col[j] = scale_byte(m);
-        if (tr == 0 && col + j < p.cols) p.st[(col + j) * p.ldst + blockIdx.y] = static_cast<uint8_t>(b_col[j]);
+        for (int w = 0; w < kQuantThreads / 32; ++w) m = larger<T>(m, column_max[w][tc * kWords + k]);
+        if constexpr (sizeof(T) == 4) {
+          b_col[k] = scale_byte(m);
+        } else {
+          b_col[2 * k] = scale_byte(as_f32_bits<T>(m & 0xffffu));
+          b_col[2 * k + 1] = scale_byte(as_f32_bits<T>(m >> 16));
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (tr == 0 && col + j < p.cols) p.st[(col + j) * p.ldst + blockIdx.y] = static_cast<uint8_t>(b_col[j]);
     }
   }
 
@@ -165,9 +265,7 @@ __global__ void __launch_bounds__(kQuantThreads) block_quantize_kernel(const __g
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t row = r0 + tr * 8 + i;
-      const float f = inverse_scale(b_row[i]);
-      const uint2 u = make_uint2(to_e4m3x4(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
-                                 to_e4m3x4(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f));
+      const uint2 u = quantize_row(v[i], inverse_scale(b_row[i]));
       if (row < p.rows && col < p.cols) store8(p.q + row * p.ldq + col, u, p.cols - col);
     }
   }
@@ -175,9 +273,9 @@ __global__ void __launch_bounds__(kQuantThreads) block_quantize_kernel(const __g
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float f = inverse_scale(b_col[j]);
-      const uint2 u = make_uint2(to_e4m3x4(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f),
-                                 to_e4m3x4(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f));
-      *reinterpret_cast<uint2*>(turned + (tc * 8 + j) * kTransposedPitch + tr * 8) = u;
+      const uint2 u = make_uint2(to_e4m3x4(v[0].at(j) * f, v[1].at(j) * f, v[2].at(j) * f, v[3].at(j) * f),
+                                 to_e4m3x4(v[4].at(j) * f, v[5].at(j) * f, v[6].at(j) * f, v[7].at(j) * f));
+      *reinterpret_cast<uint2*>(turned + turned_piece(tc * 8 + j, tr)) = u;
     }
     __syncthreads();
     // 128 rows of the transposed tile, 16 pieces of 8 bytes each
@@ -186,10 +284,21 @@ __global__ void __launch_bounds__(kQuantThreads) block_quantize_kernel(const __g
       const int row = i * 16 + tr;
       const int64_t to = c0 + row, at = r0 + tc * 8;
       if (to < p.cols && at < p.rows)
-        store8(p.qt + to * p.ldqt + at, *reinterpret_cast<const uint2*>(turned + row * kTransposedPitch + tc * 8),
-               p.rows - at);
+        store8(p.qt + to * p.ldqt + at, *reinterpret_cast<const uint2*>(turned + turned_piece(row, tc)), p.rows - at);
     }
   }
+}
+
+template <typename T>
+void launch_quantize(const QuantParams& p, int64_t row_groups, int64_t col_groups, cudaStream_t s) {
+  if (!p.whole && !p.qt) {
+    const int64_t groups = p.rows * col_groups, per_block = kRowsPerThread * kQuantThreads / 16;
+    const unsigned grid = static_cast<unsigned>((groups + per_block - 1) / per_block);
+    block_quantize_rows_kernel<T><<<grid, kQuantThreads, 0, s>>>(p);
+    return;
+  }
+  const dim3 grid(static_cast<unsigned>(col_groups), static_cast<unsigned>(row_groups));
+  block_quantize_kernel<T><<<grid, kQuantThreads, 0, s>>>(p);
 }
 
 muonh_status quant_fail(muonh_status st, const char* msg) {
@@ -207,8 +316,8 @@ extern "C" muonh_status muonh_block_quantize(const void* x, int64_t ldx, int64_t
                                              int64_t ld_scale, void* qt, int64_t ldqt, uint8_t* scale_t,
                                              int64_t ld_scale_t, void* stream) {
   set_error_message("");
-  if (rows < 0 || cols < 0 || rows > (1 << 23) || cols > INT32_MAX)
-    return quant_fail(MUONH_ERR_INVALID_ARG, "rows must be in [0, 2^23], cols in [0, 2^31 - 1]");
+  if (rows < 0 || cols < 0 || rows > 65535 * kTile || cols > INT32_MAX || rows * ((cols + kTile - 1) / kTile) > INT32_MAX)
+    return quant_fail(MUONH_ERR_INVALID_ARG, "rows must be in [0, 128 * 65535], with fewer than 2^31 groups of 128 in them");
   if (dtype != MUONH_DTYPE_F32 && dtype != MUONH_DTYPE_BF16 && dtype != MUONH_DTYPE_F16)
     return quant_fail(MUONH_ERR_INVALID_ARG, "dtype must be a MUONH_DTYPE_* type");
   if (block_rows != 1 && block_rows != kTile) return quant_fail(MUONH_ERR_INVALID_ARG, "block_rows must be 1 or 128");
@@ -239,14 +348,13 @@ extern "C" muonh_status muonh_block_quantize(const void* x, int64_t ldx, int64_t
   p.ldst = ld_scale_t;
   p.whole = block_rows == kTile;
   p.vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (rows == 1 || ldx * size % 16 == 0) && cols % 8 == 0;
-  const dim3 grid(static_cast<unsigned>(col_groups), static_cast<unsigned>(row_groups));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == MUONH_DTYPE_F32)
-    block_quantize_kernel<float><<<grid, kQuantThreads, 0, s>>>(p);
+    launch_quantize<float>(p, row_groups, col_groups, s);
   else if (dtype == MUONH_DTYPE_BF16)
-    block_quantize_kernel<__nv_bfloat16><<<grid, kQuantThreads, 0, s>>>(p);
+    launch_quantize<__nv_bfloat16>(p, row_groups, col_groups, s);
   else
-    block_quantize_kernel<__half><<<grid, kQuantThreads, 0, s>>>(p);
+    launch_quantize<__half>(p, row_groups, col_groups, s);
   if (cudaGetLastError() != cudaSuccess) return quant_fail(MUONH_ERR_CUDA, "launch of block_quantize_kernel failed");
   return MUONH_OK;
 }

@@ -9,9 +9,10 @@
 // Everything is bound by HBM: the forward pass reads x and writes y once, the
 // backward pass reads dy and x and writes dx once.  A group of G threads (8
 // lanes of a warp up to a block of 512) holds one row in registers, so a row is
-// read once whatever the number of reductions over it; groups walk over the
-// rows, and keep the weight's and, backward, the dw/db sums of their columns in
-// registers too.  Backward, the groups of a block join their sums in shared
+// read once whatever the number of reductions over it, and loads its next row
+// before it reduces the present one.  The weight is read from L1 for every row
+// (kept in registers, it cost half of the rows in flight); backward, the dw/db
+// sums of a thread's columns stay in registers.  Backward, the groups of a block join their sums in shared
 // memory, each block writes one partial row, and a second small kernel adds the
 // partial rows in a fixed order: no atomics, the same bits every time.  Rows
 // wider than the registers hold (kWide) are walked over in global memory, and
@@ -63,19 +64,26 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// V consecutive elements from a 16-byte aligned address (V = 1: any address).
+// V consecutive elements from a 16-byte aligned address (V = 1: any address),
+// as loaded and as fp32.
 template <typename T, int V>
-__device__ __forceinline__ void load_pack(const T* p, float* v) {
-  if constexpr (V == 1) {
-    v[0] = to_f(*p);
-  } else {
-    static_assert(V * sizeof(T) == 16, "a pack is one 16-byte vector");
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void to(float* v) const {
     const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = to_f(e[i]);
   }
-}
+};
+template <typename T>
+struct Raw<T, 1> {
+  T u;
+  __device__ __forceinline__ void load(const T* p) { u = *p; }
+  __device__ __forceinline__ void zero() { u = from_f<T>(0.f); }
+  __device__ __forceinline__ void to(float* v) const { v[0] = to_f(u); }
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T* p, const float* v) {
   if constexpr (V == 1) {
@@ -88,11 +96,21 @@ __device__ __forceinline__ void store_pack(T* p, const float* v) {
     *reinterpret_cast<uint4*>(p) = u;
   }
 }
-// V fp32 values of a weight-like array (its base need only be 4-byte aligned).
+// V fp32 values of a weight-like array, 16-byte aligned where V > 1; `none` without one.
 template <int V>
-__device__ __forceinline__ void load_f32(const float* p, float* v) {
+__device__ __forceinline__ void load_f32(const float* p, int64_t j, float none, float* v) {
+  if (!p) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = __ldg(p + i);
+    for (int i = 0; i < V; ++i) v[i] = none;
+  } else if constexpr (V == 1) {
+    v[0] = __ldg(p + j);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p + j + i));
+      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+  }
 }
 
 // Sums of a and b over the `group` threads of a row, in every thread of it.
@@ -131,42 +149,49 @@ __device__ __forceinline__ GroupSum group_sum(float2* shared, int group) {
 }
 
 template <typename T, int V, int P>
-__global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 sums[8 * 32];
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
   GroupSum total = group_sum(sums, G);
+  const float inv_n = 1.f / n;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
   float w[P * V], b[P * V];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
     const int j = (k * G + t) * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[k * V + i] = 1.f, b[k * V + i] = 0.f;
-    if (j < n && p.weight) load_f32<V>(p.weight + j, w + k * V);
-    if (j < n && p.bias) load_f32<V>(p.bias + j, b + k * V);
+    if (j < n) {
+      load_f32<V>(p.weight, j, 1.f, w + k * V);
+      load_f32<V>(p.bias, j, 0.f, b + k * V);
+    }
   }
-  const float inv_n = 1.f / n;
-  // the loop's bound is the block's, so that every lane takes part in the shuffles
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_block; base < p.rows;
-       base += static_cast<int64_t>(gridDim.x) * per_block) {
-    const int64_t row = base + threadIdx.x / G;
-    const bool live = row < p.rows;
+  Raw<T, V> next[P];
+  auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    float v[P * V];
-    float s = 0.f, unused = 0.f;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const int j = (k * G + t) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k * V + i] = 0.f;
-      if (live && j < n) load_pack<T, V>(x + j, v + k * V);
+      if (row < p.rows && j < n)
+        next[k].load(x + j);
+      else
+        next[k].zero();
     }
-    float mu = 0.f;
+  };
+  int64_t base = static_cast<int64_t>(blockIdx.x) * per_block;
+  fetch(base + threadIdx.x / G);
+  // the loop's bound is the block's, so that every lane takes part in the shuffles
+  for (; base < p.rows; base += step) {
+    const int64_t row = base + threadIdx.x / G;
+    float v[P * V];
+#pragma unroll
+    for (int k = 0; k < P; ++k) next[k].to(v + k * V);
+    fetch(row + step);
+    float mu = 0.f, unused = 0.f;
     if (p.mean) {
 #pragma unroll
-      for (int i = 0; i < P * V; ++i) s += v[i];
-      total(s, unused);
-      mu = s * inv_n;
+      for (int i = 0; i < P * V; ++i) mu += v[i];
+      total(mu, unused);
+      mu *= inv_n;
     }
     float q = 0.f;
 #pragma unroll
@@ -182,7 +207,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const __grid
     unused = 0.f;
     total(q, unused);
     const float rstd = 1.f / sqrtf(fmaf(q, inv_n, p.eps));
-    if (!live) continue;
+    if (row >= p.rows) continue;
     T* y = static_cast<T*>(p.out) + row * p.ldo;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
@@ -201,59 +226,73 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const __grid
   }
 }
 
-template <typename T, int V, int P>
-__global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(const __grid_constant__ NormParams p) {
+// SUMS: also the partial rows of dw and db.
+template <typename T, int V, int P, bool SUMS>
+__global__ void __launch_bounds__(kNormThreads, SUMS ? 1 : 2) norm_backward_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 sums[8 * 32];
   // [kNormThreads / G][n], where a block has several groups: at most kWide floats, 32 KB
   extern __shared__ float joined[];
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
   GroupSum total = group_sum(sums, G);
-  float w[P * V], dw[P * V], db[P * V];
+  float dw[P * V], db[P * V];
 #pragma unroll
-  for (int k = 0; k < P; ++k) {
-    const int j = (k * G + t) * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[k * V + i] = 1.f, dw[k * V + i] = 0.f, db[k * V + i] = 0.f;
-    if (j < n && p.weight) load_f32<V>(p.weight + j, w + k * V);
-  }
+  for (int i = 0; i < P * V; ++i) dw[i] = db[i] = 0.f;
   const float inv_n = 1.f / n;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_block; base < p.rows;
-       base += static_cast<int64_t>(gridDim.x) * per_block) {
-    const int64_t row = base + threadIdx.x / G;
-    const bool live = row < p.rows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  Raw<T, V> next_x[P], next_dy[P];
+  float next_mean = 0.f, next_rstd = 0.f;
+  auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-    float v[P * V], g[P * V];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const int j = (k * G + t) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k * V + i] = g[k * V + i] = 0.f;
-      if (live && j < n) {
-        load_pack<T, V>(x + j, v + k * V);
-        load_pack<T, V>(dy + j, g + k * V);
+      if (row < p.rows && j < n) {
+        next_x[k].load(x + j);
+        next_dy[k].load(dy + j);
+      } else {
+        next_x[k].zero();
+        next_dy[k].zero();
       }
     }
-    const float rstd = live ? p.rstd[row] : 0.f;
-    const float mu = (live && p.mean) ? p.mean[row] : 0.f;
+    next_rstd = row < p.rows ? p.rstd[row] : 0.f;
+    next_mean = row < p.rows && p.mean ? p.mean[row] : 0.f;
+  };
+  int64_t base = static_cast<int64_t>(blockIdx.x) * per_block;
+  fetch(base + threadIdx.x / G);
+  for (; base < p.rows; base += step) {
+    const int64_t row = base + threadIdx.x / G;
+    const float rstd = next_rstd, mu = next_mean;
+    float v[P * V], g[P * V];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      next_x[k].to(v + k * V);
+      next_dy[k].to(g + k * V);
+    }
+    fetch(row + step);
     float sg = 0.f, sgx = 0.f;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      if (live && (k * G + t) * V < n) {
+      const int j = (k * G + t) * V;
+      if (row < p.rows && j < n) {
+        float w[V];
+        load_f32<V>(p.weight, j, 1.f, w);
 #pragma unroll
         for (int i = k * V; i < (k + 1) * V; ++i) {
           v[i] = (v[i] - mu) * rstd;
-          dw[i] = fmaf(g[i], v[i], dw[i]);
-          db[i] += g[i];
-          g[i] *= w[i];
+          if (SUMS) {
+            dw[i] = fmaf(g[i], v[i], dw[i]);
+            db[i] += g[i];
+          }
+          g[i] *= w[i - k * V];
           sg += g[i];
           sgx = fmaf(g[i], v[i], sgx);
         }
       }
     }
     total(sg, sgx);
-    if (!live) continue;
+    if (row >= p.rows) continue;
     const float mg = p.mean ? sg * inv_n : 0.f, mgx = sgx * inv_n;
     T* dx = static_cast<T*>(p.out) + row * p.ldo;
 #pragma unroll
@@ -268,7 +307,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(const __gri
     }
   }
   // one partial row of dw and of db per block
-  for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < (SUMS ? 2 : 0); ++which) {
     float* part = which ? p.part_b : p.part_w;
     if (!part) continue;
     part += static_cast<int64_t>(blockIdx.x) * n;
@@ -431,45 +470,57 @@ int group_for(int64_t n, int most) {
 
 bool bad_dtype(int32_t d) { return d != MUONH_DTYPE_F32 && d != MUONH_DTYPE_BF16 && d != MUONH_DTYPE_F16; }
 
+enum Pass { kForward, kBackward, kBackwardRows };   // kBackwardRows: dx alone
+
 template <typename T, int V, int P>
-cudaError_t launch_row(const NormParams& p, bool backward, int grid, size_t smem, cudaStream_t s) {
-  if (backward) {
-    norm_backward_kernel<T, V, P><<<grid, kNormThreads, smem, s>>>(p);
-  } else {
+cudaError_t launch_row(const NormParams& p, Pass pass, int grid, size_t smem, cudaStream_t s) {
+  if (pass == kForward)
     norm_forward_kernel<T, V, P><<<grid, kNormThreads, 0, s>>>(p);
-  }
+  else if (pass == kBackward)
+    norm_backward_kernel<T, V, P, true><<<grid, kNormThreads, smem, s>>>(p);
+  else
+    norm_backward_kernel<T, V, P, false><<<grid, kNormThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_typed(NormParams p, bool backward, bool vec, int elems, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_typed(NormParams p, Pass pass, bool vec, int elems, int grid, size_t smem, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   if (vec) {
-    if (elems <= V) return launch_row<T, V, 1>(p, backward, grid, smem, s);
-    if (elems <= 8) return launch_row<T, V, 8 / V>(p, backward, grid, smem, s);
-    return launch_row<T, V, 16 / V>(p, backward, grid, smem, s);
+    if (elems <= V) return launch_row<T, V, 1>(p, pass, grid, smem, s);
+    if (elems <= 8) return launch_row<T, V, 8 / V>(p, pass, grid, smem, s);
+    return launch_row<T, V, 16 / V>(p, pass, grid, smem, s);
   }
-  if (elems <= 4) return launch_row<T, 1, 4>(p, backward, grid, smem, s);
-  if (elems <= 8) return launch_row<T, 1, 8>(p, backward, grid, smem, s);
-  return launch_row<T, 1, 16>(p, backward, grid, smem, s);
+  if (elems <= 4) return launch_row<T, 1, 4>(p, pass, grid, smem, s);
+  if (elems <= 8) return launch_row<T, 1, 8>(p, pass, grid, smem, s);
+  return launch_row<T, 1, 16>(p, pass, grid, smem, s);
 }
 
-cudaError_t launch(const NormParams& p, int32_t dtype, bool backward, bool vec, int elems, int grid, size_t smem,
+cudaError_t launch(const NormParams& p, int32_t dtype, Pass pass, bool vec, int elems, int grid, size_t smem,
                    cudaStream_t s) {
-  if (dtype == MUONH_DTYPE_F32) return launch_typed<float>(p, backward, vec, elems, grid, smem, s);
-  if (dtype == MUONH_DTYPE_BF16) return launch_typed<__nv_bfloat16>(p, backward, vec, elems, grid, smem, s);
-  return launch_typed<__half>(p, backward, vec, elems, grid, smem, s);
+  if (dtype == MUONH_DTYPE_F32) return launch_typed<float>(p, pass, vec, elems, grid, smem, s);
+  if (dtype == MUONH_DTYPE_BF16) return launch_typed<__nv_bfloat16>(p, pass, vec, elems, grid, smem, s);
+  return launch_typed<__half>(p, pass, vec, elems, grid, smem, s);
+}
+
+// Partial rows of dw and db from x and dy: a thread per column, `slices` shares of the rows.
+cudaError_t launch_columns(const NormParams& p, int32_t dtype, int slices, cudaStream_t s) {
+  const dim3 grid((p.n + 255) / 256, slices);
+  if (dtype == MUONH_DTYPE_F32)
+    norm_columns_kernel<float><<<grid, 256, 0, s>>>(p);
+  else if (dtype == MUONH_DTYPE_BF16)
+    norm_columns_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  else
+    norm_columns_kernel<__half><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_wide(const NormParams& p, bool backward, int grid, int slices, cudaStream_t s) {
-  if (!backward) {
+cudaError_t launch_wide(const NormParams& p, Pass pass, int grid, cudaStream_t s) {
+  if (pass == kForward)
     norm_forward_wide_kernel<T><<<grid, kNormThreads, 0, s>>>(p);
-  } else {
+  else
     norm_backward_wide_kernel<T><<<grid, kNormThreads, 0, s>>>(p);
-    if (slices > 0)
-      norm_columns_kernel<T><<<dim3((p.n + 255) / 256, slices), 256, 0, s>>>(p);
-  }
   return cudaGetLastError();
 }
 
@@ -478,6 +529,8 @@ muonh_status check_rows(int64_t rows, int64_t n, int32_t dtype) {
     return norm_fail(MUONH_ERR_INVALID_ARG, "need rows >= 0, 1 <= n < 2^31 - 512 and a MUONH_DTYPE_* type");
   return MUONH_OK;
 }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The kernels move single elements where a row is not 16-byte aligned.
 bool misaligned(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; }
@@ -516,16 +569,17 @@ extern "C" muonh_status muonh_layer_norm(const void* x, int64_t ldx, void* y, in
   cudaError_t e;
   if (n > kWide) {
     const int grid = static_cast<int>(std::min<int64_t>(rows, 4ll * sm_count()));
-    e = dtype == MUONH_DTYPE_F32    ? launch_wide<float>(p, false, grid, 0, s)
-        : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, false, grid, 0, s)
-                                    : launch_wide<__half>(p, false, grid, 0, s);
+    e = dtype == MUONH_DTYPE_F32    ? launch_wide<float>(p, kForward, grid, s)
+        : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, kForward, grid, s)
+                                    : launch_wide<__half>(p, kForward, grid, s);
   } else {
-    const bool vec = packed(x, ldx, n, size) && packed(y, ldy, n, size);
-    p.group = group_for(n, kMaxPack);
+    const bool vec = packed(x, ldx, n, size) && packed(y, ldy, n, size) && aligned16(weight) && aligned16(bias);
+    // 8 elements per thread leave room for three blocks per SM
+    p.group = group_for(n, n <= kNormThreads * 8 ? 8 : kMaxPack);
     const int elems = static_cast<int>((n + p.group - 1) / p.group);
     const int64_t blocks = (rows + kNormThreads / p.group - 1) / (kNormThreads / p.group);
-    const int grid = static_cast<int>(std::min<int64_t>(blocks, 4ll * sm_count()));
-    e = launch(p, dtype, false, vec, elems, grid, 0, s);
+    const int grid = static_cast<int>(std::min<int64_t>(blocks, (elems <= 8 ? 3ll : 1ll) * sm_count()));   // all at once
+    e = launch(p, dtype, kForward, vec, elems, grid, 0, s);
   }
   if (e != cudaSuccess) return norm_fail(MUONH_ERR_CUDA, "launch of the layer norm kernel failed");
   return MUONH_OK;
@@ -579,27 +633,41 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
   int parts;
   cudaError_t e;
   float* part = static_cast<float*>(workspace);
-  if (n > kWide) {
-    parts = sums ? static_cast<int>(std::min<int64_t>(rows, 64)) : 0;
+  const bool vec = packed(x, ldx, n, size) && packed(dy, lddy, n, size) && packed(dx, lddx, n, size) &&
+                   aligned16(weight);
+  // the column sums of 16 elements per thread fit next to a prefetched row
+  // only where both rows are packed 16-bit; else they come from a kernel of
+  // their own (x and dy are then read twice, the second time mostly from L2)
+  const int most = vec && size == 2 ? kMaxPack : 8;
+  const bool split = sums && n > static_cast<int64_t>(kNormThreads) * most;
+  auto set_parts = [&](int count) {   // a single partial row is the result
+    parts = count;
     if (dweight) p.part_w = parts == 1 ? dweight : part;
     if (dbias) p.part_b = parts == 1 ? dbias : part + static_cast<int64_t>(parts) * n;
+  };
+  parts = 0;
+  if (n > kWide) {
     const int grid = static_cast<int>(std::min<int64_t>(rows, 4ll * sms));
-    e = dtype == MUONH_DTYPE_F32    ? launch_wide<float>(p, true, grid, parts, s)
-        : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, true, grid, parts, s)
-                                    : launch_wide<__half>(p, true, grid, parts, s);
+    e = dtype == MUONH_DTYPE_F32    ? launch_wide<float>(p, kBackward, grid, s)
+        : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, kBackward, grid, s)
+                                    : launch_wide<__half>(p, kBackward, grid, s);
   } else {
-    const bool vec = packed(x, ldx, n, size) && packed(dy, lddy, n, size) && packed(dx, lddx, n, size);
-    p.group = group_for(n, kMaxPack);
+    p.group = group_for(n, split || !sums ? kMaxPack : most);
     const int elems = static_cast<int>((n + p.group - 1) / p.group);
     const int per_block = kNormThreads / p.group;
     const int64_t blocks = (rows + per_block - 1) / per_block;
-    const int grid = static_cast<int>(std::min<int64_t>({blocks, 2ll * sms, static_cast<int64_t>(kMaxParts)}));
-    parts = grid;
-    // a single block's sums are the result
-    if (dweight) p.part_w = parts == 1 ? dweight : part;
-    if (dbias) p.part_b = parts == 1 ? dbias : part + static_cast<int64_t>(parts) * n;
-    const size_t smem = (sums && per_block > 1) ? static_cast<size_t>(per_block) * n * sizeof(float) : 0;
-    e = launch(p, dtype, true, vec, elems, grid, smem, s);
+    if (split || !sums) {
+      e = launch(p, dtype, kBackwardRows, vec, elems, static_cast<int>(std::min<int64_t>(blocks, 2ll * sms)), 0, s);
+    } else {
+      const int grid = static_cast<int>(std::min<int64_t>({blocks, sms, static_cast<int64_t>(kMaxParts)}));
+      set_parts(grid);
+      const size_t smem = per_block > 1 ? static_cast<size_t>(per_block) * n * sizeof(float) : 0;
+      e = launch(p, dtype, kBackward, vec, elems, grid, smem, s);
+    }
+  }
+  if (e == cudaSuccess && split) {
+    set_parts(static_cast<int>(std::min<int64_t>(rows, 64)));
+    e = launch_columns(p, dtype, parts, s);
   }
   if (e == cudaSuccess && sums && parts > 1) {
     norm_join_kernel<<<dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1), 32 * kJoinSlices, 0, s>>>(

@@ -32,6 +32,7 @@
 // accumulated in TMEM before they are added in IEEE fp32 registers.
 // The result is rounded once to X's type.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "muonh_common.cuh"
@@ -635,6 +636,44 @@ muonh_status check_orth(const muonh_orthogonalize_desc* d) {
   return MUONH_OK;
 }
 
+// Clusters of `ranks` CTAs that the device holds at once.  A cluster has to fit
+// in one GPC, so fewer of the large ones fit than the SMs alone would say: 16
+// clusters of 8 took two waves and 100 us where 16 of 4 took 57.
+int clusters_at_once(bool bf16, int ranks, int dev) {
+  static std::atomic<int> known[64][4];          // per device and log2(ranks), plus one
+  int log = 0;
+  while ((1 << log) < ranks) ++log;
+  std::atomic<int>* memo = dev >= 0 && dev < 64 ? &known[dev][log] : nullptr;
+  if (memo && memo->load()) return memo->load() - 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+  cfg.blockDim = dim3(kOrthThreads);
+  cfg.dynamicSmemBytes = kOrthSmem;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e = bf16 ? cudaOccupancyMaxActiveClusters(&n, orthogonalize_kernel<true>, &cfg)
+                             : cudaOccupancyMaxActiveClusters(&n, orthogonalize_kernel<false>, &cfg);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (memo) memo->store(n + 1);
+  return n;
+}
+
+// More CTAs per matrix while all clusters still run at once and each CTA has
+// two slices at least.
+int pick_cluster(bool bf16, int64_t batch, int slices, int dev) {
+  int ranks = 1;
+  while (ranks < kMaxCluster && slices >= 4 * ranks && batch <= clusters_at_once(bf16, 2 * ranks, dev)) ranks *= 2;
+  return ranks;
+}
+
 size_t copy_bytes(const muonh_orthogonalize_desc& d) {
   return static_cast<size_t>(d.batch) * d.rows * up8(d.cols) * 2;
 }
@@ -691,14 +730,15 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   p.eps = d->eps;
   ns_chain_scales(p.a, p.b, p.c, p.steps, &p.ea, &p.eb, p.eq);
   p.eq_last = (d->dtype == MUONH_DTYPE_BF16 || p.steps == 0) ? 0 : p.eq[p.steps - 1];
-  // more CTAs per matrix while that leaves none of them waiting for an SM and
-  // each has two slices at least
-  int ranks = 1;
-  while (ranks < kMaxCluster && d->batch * ranks * 2 <= sms && p.slices >= 4 * ranks) ranks *= 2;
-
   CUtensorMap xmap, omap;
   if (!encode_stack(&xmap, in, *d, kSide) || !encode_stack(&omap, out, *d, 32))
     return orth_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const bool bf16 = d->dtype == MUONH_DTYPE_BF16;
+  cudaError_t e = bf16 ? cudaFuncSetAttribute(orthogonalize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kOrthSmem)
+                       : cudaFuncSetAttribute(orthogonalize_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              kOrthSmem);
+  const int ranks = pick_cluster(bf16, d->batch, p.slices, dev);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(d->batch * ranks));
   cfg.blockDim = dim3(kOrthThreads);
@@ -710,11 +750,6 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const bool bf16 = d->dtype == MUONH_DTYPE_BF16;
-  cudaError_t e = bf16 ? cudaFuncSetAttribute(orthogonalize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kOrthSmem)
-                       : cudaFuncSetAttribute(orthogonalize_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kOrthSmem);
   if (e == cudaSuccess)
     e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
              : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);

@@ -5,19 +5,26 @@ Like the rest of the binding these calls check and marshal arguments; the work
 is in the library's CUDA kernels.  Each call runs on the device of its tensors,
 on `stream` or that device's current stream.  A given stream is also the one
 that results and scratch are allocated on, as under `torch.cuda.stream(stream)`.
+
+The smallest calls are bound by the host, so the usual case (the current stream
+of the current device) takes no context manager and no Stream object.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
-from .muonh import DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, BlockOperand, OrthogonalizeDesc, _check, library
+from .muonh import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, BlockOperand, OrthogonalizeDesc, _check, library)
+
+_TYPES = None
 
 
-def _dtype_code(dtype):
-    import torch
-    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-    return codes.get(dtype)
+def _types():
+    """{torch dtype: MUONH_DTYPE_*}; torch is imported with the first call, like elsewhere in the binding."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    return _TYPES
 
 
 def _tensor(t, what: str, dtypes, device=None):
@@ -26,42 +33,38 @@ def _tensor(t, what: str, dtypes, device=None):
         raise TypeError(f"{what} must be a CUDA tensor of dtype {', '.join(map(str, dtypes))}")
     if device is not None and t.device != device:
         raise ValueError(f"{what} must be on {device}, like the other tensors")
-    return t
 
 
-@contextlib.contextmanager
-def _on_other(device, stream):
+def _here(t, stream):
+    """The handle of the current stream where the call belongs there; None where it has to move first."""
     import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    index = t.get_device()
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
 
 
-def _on(device, stream):
-    """Context in which a call's allocations and launches belong to `device` and
-    `stream`; gives the stream's handle."""
+def _elsewhere(device, stream, call, *args, **kw):
+    """`call` with `device` and `stream` as the current ones."""
     import torch
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext(torch.cuda.current_stream().cuda_stream)
-    return _on_other(device, stream)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must belong to {device}, like the tensors")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _rows(t, what: str):
     """(pointer, rows, n, row stride) of a tensor seen as rows of its last
     dimension; ValueError where one stride does not lead from row to row."""
-    n = t.shape[-1]
-    rows = 1
-    for d in t.shape[:-1]:
-        rows *= d
+    shape = t.shape
+    n = shape[-1]
     if t.is_contiguous():
-        return t.data_ptr(), rows, n, n
+        return t.data_ptr(), (shape[0] if len(shape) == 2 else shape[:-1].numel()), n, n
     if n > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    ld, expect = None, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    rows, ld, expect = 1, None, None
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        rows *= size
         if size == 1:
             continue
         if ld is None:
@@ -92,23 +95,29 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     `out`, which may be x), mean (None for the RMS norm) and rstd fp32, one per
     row, for layer_norm_backward."""
     import torch
-    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    _tensor(x, "x", _types())
+    handle = _here(x, stream)
+    if handle is None:
+        return _elsewhere(x.device, stream, layer_norm, x, weight, bias, eps, rms, out)
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must have a last dimension of at least one element")
+    device, dtype, lead = x.device, x.dtype, x.shape[:-1]
     xp, rows, n, ldx = _rows(x, "x")
-    wp = _vector(weight, "weight", n, x.device)
-    bp = _vector(bias, "bias", n, x.device)
-    with _on(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _tensor(out, "out", (x.dtype,), x.device)
+    wp = _vector(weight, "weight", n, device)
+    bp = _vector(bias, "bias", n, device)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, ldo = out.data_ptr(), n
+    else:
+        _tensor(out, "out", (dtype,), device)
         if out.shape != x.shape:
             raise ValueError("out must have x's shape")
         op, _, _, ldo = _rows(out, "out")
-        mean = None if rms else torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(library().muonh_layer_norm(xp, ldx, op, ldo, wp, bp, None if rms else mean.data_ptr(),
-                                          rstd.data_ptr(), rows, n, _dtype_code(x.dtype), eps, handle))
+    lead = lead or ((),)   # torch.empty(*sizes) costs half of torch.empty(size)
+    mean = None if rms else torch.empty(*lead, dtype=torch.float32, device=device)
+    rstd = torch.empty(*lead, dtype=torch.float32, device=device)
+    _check(library().muonh_layer_norm(xp, ldx, op, ldo, wp, bp, None if rms else mean.data_ptr(), rstd.data_ptr(),
+                                      rows, n, _types()[dtype], eps, handle))
     return out, mean, rstd
 
 
@@ -118,100 +127,116 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
     mean None means the RMS norm.  dweight (None where weight is None) and dbias
     (None unless bias is true) are fp32, as adamw_step reads them."""
     import torch
-    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
-    _tensor(dy, "dy", (x.dtype,), x.device)
+    _tensor(x, "x", _types())
+    handle = _here(x, stream)
+    if handle is None:
+        return _elsewhere(x.device, stream, layer_norm_backward, dy, x, weight, mean, rstd, bias)
+    device, dtype = x.device, x.dtype
+    _tensor(dy, "dy", (dtype,), device)
     if x.dim() < 1 or x.shape[-1] < 1 or dy.shape != x.shape:
         raise ValueError("dy and x must have the same shape, with a last dimension of at least one element")
     xp, rows, n, ldx = _rows(x, "x")
     dyp, _, _, lddy = _rows(dy, "dy")
-    wp = _vector(weight, "weight", n, x.device)
-    mp = _vector(mean, "mean", rows, x.device)
-    rp = _vector(rstd, "rstd", rows, x.device)
+    wp = _vector(weight, "weight", n, device)
+    mp = _vector(mean, "mean", rows, device)
+    rp = _vector(rstd, "rstd", rows, device)
     if rp is None:
         raise TypeError("rstd must be given")
     lib = library()
-    with _on(x.device, stream) as handle:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dweight = None if weight is None else torch.empty(weight.shape, dtype=torch.float32, device=x.device)
-        dbias = torch.empty(n, dtype=torch.float32, device=x.device) if bias else None
-        size = lib.muonh_layer_norm_workspace(rows, n) if weight is not None or bias else 0
-        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-        _check(lib.muonh_layer_norm_backward(
-            dyp, lddy, xp, ldx, wp, mp, rp, dx.data_ptr(), n, None if dweight is None else dweight.data_ptr(),
-            None if dbias is None else dbias.data_ptr(), rows, n, _dtype_code(x.dtype),
-            None if work is None else work.data_ptr(), size, handle))
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = torch.empty(n, dtype=torch.float32, device=device) if bias else None
+    size = lib.muonh_layer_norm_workspace(rows, n) if weight is not None or bias else 0
+    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    _check(lib.muonh_layer_norm_backward(
+        dyp, lddy, xp, ldx, wp, mp, rp, dx.data_ptr(), n, None if dweight is None else dweight.data_ptr(),
+        None if dbias is None else dbias.data_ptr(), rows, n, _types()[dtype],
+        None if work is None else work.data_ptr(), size, handle))
     return dx, dweight, dbias
 
 
 def _stack(t, what: str):
     """(pointer, matrix stride, row stride) of a 2-D or 3-D tensor as a stack of matrices."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, strides = t.shape, t.stride()
+    rows, cols = shape[-2], shape[-1]
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{what} must have unit column stride")
-    if t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+    if rows > 1 and strides[-2] < cols:
         raise ValueError(f"{what} must have rows that do not overlap")
-    return t.data_ptr(), t.stride(0) if t.dim() == 3 else 0, max(t.stride(-2), t.shape[-1])
+    return t.data_ptr(), strides[0] if len(shape) == 3 else 0, max(strides[-2], cols)
 
 
 def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, stream=None):
     """The Newton-Schulz output of each matrix of a stack x ([rows, cols] or
     [batch, rows, cols], bf16 or fp16, unit column stride, any other strides),
     for matrices whose smaller side is at most 128: one Muon update per
-    attention head.  Returns a tensor of x's shape and type, or `out`, which
-    may be x."""
+    attention head.  Returns a tensor of x's shape and type, laid out like x
+    where x has no gaps, or `out`, which may be x."""
     import torch
     _tensor(x, "x", (torch.bfloat16, torch.float16))
-    if x.dim() not in (2, 3):
+    handle = _here(x, stream)
+    if handle is None:
+        return _elsewhere(x.device, stream, orthogonalize, x, ns_steps=ns_steps, ns_coeffs=ns_coeffs, eps=eps, out=out)
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be a matrix or a stack of matrices")
     xp, xs, ldx = _stack(x, "x")
     a, b, c = ns_coeffs
-    rows, cols = x.shape[-2:]
+    batch = shape[0] if len(shape) == 3 else 1
+    rows, cols = shape[-2], shape[-1]
     lib = library()
-    with _on(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
         _tensor(out, "out", (x.dtype,), x.device)
-        if out.shape != x.shape:
+        if out.shape != shape:
             raise ValueError("out must have x's shape")
-        op, os_, ldo = _stack(out, "out")
-        if x.dim() == 3 and x.shape[0] > 1 and os_ < cols:
-            raise ValueError("out must have matrices that do not overlap")
-        d = OrthogonalizeDesc(xp, op, x.shape[0] if x.dim() == 3 else 1, rows, cols, xs, ldx, os_, ldo,
-                              _dtype_code(x.dtype), int(ns_steps), a, b, c, eps)
-        size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))
-        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-        _check(lib.muonh_orthogonalize(ctypes.byref(d), None if work is None else work.data_ptr(), size, handle))
+    op, os_, ldo = _stack(out, "out")
+    if batch > 1 and os_ < cols:
+        raise ValueError("out must have matrices that do not overlap")
+    d = OrthogonalizeDesc(xp, op, batch, rows, cols, xs, ldx, os_, ldo, _types()[x.dtype], int(ns_steps), a, b, c, eps)
+    size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))
+    work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+    _check(lib.muonh_orthogonalize(ctypes.byref(d), None if work is None else work.data_ptr(), size, handle))
     return out
 
 
 def _matrix(t, what: str):
     """(pointer, rows, cols, row stride) of a 2-D tensor with unit column stride."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be 2-D")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what} must have unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows > 1 and ld < cols:
         raise ValueError(f"{what} must have rows that do not overlap")
-    return t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1])
+    return t.data_ptr(), rows, cols, ld if ld > cols else cols
 
 
 def _quantize(x, block_rows, rows, columns, stream):
     import torch
-    _tensor(x, "x", (torch.float32, torch.bfloat16, torch.float16))
+    _tensor(x, "x", _types())
+    handle = _here(x, stream)
+    if handle is None:
+        return _elsewhere(x.device, stream, _quantize, x, block_rows, rows, columns, None)
+    device = x.device
     xp, m, n, ldx = _matrix(x, "x")
     out = []
 
     def room(r, c):
         """r x c bytes with a row stride that is a multiple of 16, and their scales."""
         ld, groups = -(-c // 16) * 16, -(-c // 128)
-        q = torch.empty((r, ld), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((-(-r // block_rows), groups), dtype=torch.uint8, device=x.device)
-        out.extend((q if ld == c else q[:, :c], s))
+        q = torch.empty(r, ld, dtype=torch.float8_e4m3fn, device=device)
+        s = torch.empty(-(-r // block_rows), groups, dtype=torch.uint8, device=device)
+        out.append(q if ld == c else q[:, :c])
+        out.append(s)
         return q.data_ptr(), ld, s.data_ptr(), groups
 
-    with _on(x.device, stream) as handle:
-        args = room(m, n) if rows else (None, 0, None, 0)
-        args += room(n, m) if columns else (None, 0, None, 0)
-        _check(library().muonh_block_quantize(xp, ldx, m, n, _dtype_code(x.dtype), block_rows, *args, handle))
+    args = room(m, n) if rows else (None, 0, None, 0)
+    args += room(n, m) if columns else (None, 0, None, 0)
+    _check(library().muonh_block_quantize(xp, ldx, m, n, _types()[x.dtype], block_rows, *args, handle))
     return tuple(out)
 
 
@@ -232,13 +257,13 @@ def block_quantize_weight(w, stream=None):
     return _quantize(w, 128, True, True, stream)
 
 
-def _block_operand(q, scale, what: str, device):
+def _block_operand(q, scale, what: str, device=None):
     import torch
     _tensor(q, what, (torch.float8_e4m3fn,), device)
-    _tensor(scale, f"{what}_scale", (torch.uint8,), device)
+    _tensor(scale, f"{what}_scale", (torch.uint8,), q.device)
     qp, rows, k, ld = _matrix(q, what)
     sp, srows, groups, lds = _matrix(scale, f"{what}_scale")
-    if groups != -(-k // 128) or srows not in (rows, -(-rows // 128)):
+    if groups != -(-k // 128) or (srows != rows and srows != -(-rows // 128)):
         raise ValueError(f"{what}_scale must be [{rows} or {-(-rows // 128)}, {-(-k // 128)}] for {what} [{rows}, {k}]")
     return BlockOperand(qp, sp, rows, ld, lds, 1 if srows == rows else 128, 0), rows, k
 
@@ -250,28 +275,29 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
     or fp16) or writes to `out`; accumulate=True adds to an fp32 `out`, such as
     the gradient that MuonH.step reads."""
     import torch
-    ao, m, k = _block_operand(a, a_scale, "a", None)
+    ao, m, k = _block_operand(a, a_scale, "a")
+    handle = _here(a, stream)
+    if handle is None:
+        return _elsewhere(a.device, stream, block_matmul, a, a_scale, b, b_scale, dtype=dtype, out=out,
+                          accumulate=accumulate)
     bo, n, kb = _block_operand(b, b_scale, "b", a.device)
-    _tensor(a_scale, "a_scale", (torch.uint8,), a.device)
     if k != kb:
         raise ValueError("a and b must have the same number of columns")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         dtype = torch.bfloat16 if dtype is None else dtype
-    elif dtype is not None and dtype != out.dtype:
-        raise ValueError("out must be of dtype")
-    with _on(a.device, stream) as handle:
-        if out is None:
-            if _dtype_code(dtype) is None:
-                raise TypeError("dtype must be torch.float32, torch.bfloat16 or torch.float16")
-            out = torch.empty((m, n), dtype=dtype, device=a.device)
-        _tensor(out, "out", (torch.float32, torch.bfloat16, torch.float16), a.device)
+        if dtype not in _types():
+            raise TypeError("dtype must be torch.float32, torch.bfloat16 or torch.float16")
+        out = torch.empty(m, n, dtype=dtype, device=a.device)
+        op, ldo = out.data_ptr(), n
+    else:
+        _tensor(out, "out", _types() if dtype is None else (dtype,), a.device)
         if out.shape != (m, n):
             raise ValueError(f"out must be [{m}, {n}]")
         op, _, _, ldo = _matrix(out, "out")
-        _check(library().muonh_block_matmul(ctypes.byref(ao), ctypes.byref(bo), k, op, ldo, _dtype_code(out.dtype),
-                                            int(bool(accumulate)), handle))
+    _check(library().muonh_block_matmul(ctypes.byref(ao), ctypes.byref(bo), k, op, ldo, _types()[out.dtype],
+                                        1 if accumulate else 0, handle))
     return out
 
 
