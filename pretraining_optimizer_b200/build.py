@@ -23,7 +23,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-shared",
-         "--expt-relaxed-constexpr", "-cudart", "static"]
+         "--expt-relaxed-constexpr", "-cudart", "static", "--threads", "0"]
 
 
 def sources() -> list[str]:

@@ -250,11 +250,12 @@ bool muonh::encode_bytes(CUtensorMap* out, void* base, int64_t cols, int64_t row
 
 extern "C" muonh_status muonh_operator_status(void* stream) {
   set_error_message("");
-  int orth = 0, block = 0;
+  int orth = 0, block = 0, norm = 0;
   if (take_orth_timeout(&orth, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
-      take_block_timeout(&block, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      take_block_timeout(&block, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      take_norm_timeout(&norm, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return fail(MUONH_ERR_CUDA, "reading the operators' status failed");
-  if (orth || block) return fail(MUONH_ERR_TIMEOUT, "a device-side bounded wait gave up");
+  if (orth || block || norm) return fail(MUONH_ERR_TIMEOUT, "a device-side bounded wait gave up");
   return MUONH_OK;
 }
 

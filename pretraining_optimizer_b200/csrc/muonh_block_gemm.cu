@@ -607,12 +607,4 @@ extern "C" muonh_status muonh_block_matmul(const muonh_block_operand* a, const m
   return MUONH_OK;
 }
 
-cudaError_t muonh::take_block_timeout(int* flag, cudaStream_t s) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_block_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *flag)
-    e = cudaMemcpyToSymbolAsync(g_block_timeout, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return e;
-}
+cudaError_t muonh::take_block_timeout(int* flag, cudaStream_t s) { return take_flag(g_block_timeout, flag, s); }

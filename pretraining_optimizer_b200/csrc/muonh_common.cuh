@@ -454,9 +454,19 @@ bool encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t cols, i
 // 128 columns and box_rows rows (128-byte swizzle).
 bool encode_bytes(CUtensorMap* out, void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
-// Reads and clears the record that a bounded wait gave up; synchronises s.
+// Reads and clears the records that a bounded wait gave up, one per source
+// file with such waits; synchronises s.
 cudaError_t take_orth_timeout(int* flag, cudaStream_t s);
 cudaError_t take_block_timeout(int* flag, cudaStream_t s);
+cudaError_t take_norm_timeout(int* flag, cudaStream_t s);
+template <typename Symbol>
+cudaError_t take_flag(const Symbol& symbol, int* flag, cudaStream_t s) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, symbol, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
 
 // Message returned by muonh_last_error() on the calling thread.
 void set_error_message(const char* msg);

@@ -7,20 +7,25 @@
 // < > is the mean over the row; the RMS norm has mu = 0 and no <g> term.
 //
 // Everything is bound by HBM: the forward pass reads x and writes y once, the
-// backward pass reads dy and x and writes dx once.  A group of G threads (8
-// lanes of a warp up to a block of 512) holds one row in registers, so a row is
-// read once whatever the number of reductions over it, and loads its next row
-// before it reduces the present one.  The weight is read from L1 for every row
-// (kept in registers, it cost half of the rows in flight); backward, the dw/db
-// sums of a thread's columns stay in registers.  Backward, the groups of a block join their sums in shared
-// memory, each block writes one partial row, and a second small kernel adds the
-// partial rows in a fixed order: no atomics, the same bits every time.  Rows
-// wider than the registers hold (kWide) are walked over in global memory, and
-// dw/db then come from a kernel of their own that walks down the columns.
+// backward pass reads dy and x and writes dx once.  A group of G threads holds
+// one row in registers, so a row is read once whatever the number of reductions
+// over it, and its next rows are on their way meanwhile:
+//   up to 32 lanes per row (n <= 512)     the next row is loaded into registers
+//   128 or 512 threads per row (n <= 8192) the next rows are copied to a ring in
+//            shared memory (cp.async.bulk).  Prefetching such rows in registers
+//            spilled, or left half of the threads: 1021 x 5003 fp32 backward took
+//            57 us that way, and 35 us without any prefetch.  A row that does not
+//            start on 16 bytes is copied from the 16-byte piece that it starts in.
+//   wider    walked over in global memory; dw and db come from a kernel of their own.
+// Backward, the dw/db sums of a thread's columns stay in registers over all rows
+// of its group, the groups of a block join theirs in shared memory, each block
+// writes one partial row, and a second small kernel adds the partial rows in a
+// fixed order: no atomics, the same bits every time.
 //
 // All sums are fp32: per thread over at most 16 elements of a row, then a tree.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "muonh_common.cuh"
 
@@ -31,6 +36,9 @@ constexpr int kNormThreads = 512;
 constexpr int kMaxPack = 16;                        // elements of a row per thread
 constexpr int kWide = kNormThreads * kMaxPack;      // widest row held in registers: 8192
 constexpr int kMaxParts = 512;                      // partial rows of dw/db
+constexpr int kMaxRing = 4;                         // rows in flight per group
+
+__device__ int g_norm_timeout;                      // a wait gave up in some call since the flag was read
 
 struct NormParams {
   const void* x;
@@ -44,6 +52,7 @@ struct NormParams {
   float* part_b;
   int64_t rows, ldx, lddy, ldo;
   int32_t n, group;          // row width; threads per row
+  int32_t ring, slot;        // rows in flight per group, and the bytes of one operand's row
   float eps;
 };
 
@@ -64,38 +73,92 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// V consecutive elements from a 16-byte aligned address (V = 1: any address),
-// as loaded and as fp32.
+// Two 16-bit values of a word as fp32, and back.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// V elements in 32-bit words, as they are in memory.
 template <typename T, int V>
-struct Raw {
-  uint4 u;
-  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void to(float* v) const {
-    const T* e = reinterpret_cast<const T*>(&u);
+struct Words {
+  static constexpr int kWords = V * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {   // aligned to all of them
+    if constexpr (kWords == 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kWords == 4)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = to_f(e[i]);
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void to(float* v) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = unpack2<T>(w[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void from(const float* v) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4)
+        w[i] = __float_as_uint(v[i]);
+      else
+        w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
   }
 };
 template <typename T>
-struct Raw<T, 1> {
-  T u;
-  __device__ __forceinline__ void load(const T* p) { u = *p; }
-  __device__ __forceinline__ void zero() { u = from_f<T>(0.f); }
-  __device__ __forceinline__ void to(float* v) const { v[0] = to_f(u); }
+struct Words<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = w; }
+  __device__ __forceinline__ void zero() { w = from_f<T>(0.f); }
+  __device__ __forceinline__ void to(float* v) const { v[0] = to_f(w); }
+  __device__ __forceinline__ void from(const float* v) { w = from_f<T>(v[0]); }
 };
 template <typename T, int V>
-__device__ __forceinline__ void store_pack(T* p, const float* v) {
-  if constexpr (V == 1) {
-    *p = from_f<T>(v[0]);
-  } else {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = from_f<T>(v[i]);
-    *reinterpret_cast<uint4*>(p) = u;
-  }
+__device__ __forceinline__ void read_row(const T* p, float* v) {
+  Words<T, V> w;
+  w.load(p);
+  w.to(v);
 }
+template <typename T, int V>
+__device__ __forceinline__ void write_row(T* p, const float* v) {
+  Words<T, V> w;
+  w.from(v);
+  w.store(p);
+}
+
 // V fp32 values of a weight-like array, 16-byte aligned where V > 1; `none` without one.
 template <int V>
 __device__ __forceinline__ void load_f32(const float* p, int64_t j, float none, float* v) {
@@ -113,47 +176,61 @@ __device__ __forceinline__ void load_f32(const float* p, int64_t j, float none, 
   }
 }
 
-// Sums of a and b over the `group` threads of a row, in every thread of it.
-// Groups within a warp use shuffles; wider groups add their warps' sums in
-// shared memory behind a barrier of their own.  `buf` alternates between two
-// slots, so that one barrier per call is enough.
-struct GroupSum {
-  float2* slots;             // [2][16] of this group's warps
-  int group, bar, flip;
-  __device__ __forceinline__ void operator()(float& a, float& b) {
-    const int w = group < 32 ? group : 32;
-    for (int o = w >> 1; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (group > 32) {
-      const int warps = group >> 5, warp = (threadIdx.x % group) >> 5;
-      float2* s = slots + flip * 16;
-      flip ^= 1;
-      if ((threadIdx.x & 31) == 0) s[warp] = make_float2(a, b);
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(group) : "memory");
-      a = b = 0.f;
-      for (int i = 0; i < warps; ++i) {
-        const float2 t = s[i];
-        a += t.x;
-        b += t.y;
-      }
-    }
+// Sums over the `group` lanes (up to 32) of a row, in each of them.
+__device__ __forceinline__ float lane_sum(float a, int group) {
+  for (int o = group >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
+}
+__device__ __forceinline__ void lane_sum(float& a, float& b, int group) {
+  for (int o = group >> 1; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
   }
-};
-
-__device__ __forceinline__ GroupSum group_sum(float2* shared, int group) {
-  const int g = threadIdx.x / group;
-  // wider groups than a warp: at most 8 of 64 threads, barrier ids 1..8
-  return GroupSum{group > 32 ? shared + 32 * g : shared, group, 1 + (group > 32 ? g : 0), 0};
 }
 
+// Sums over the G threads (whole warps) of a row, in every thread of it: within
+// the warps by shuffles, then over the warps in shared memory behind a barrier
+// of the group's own.  Two slots alternate, so that one barrier per call is enough.
+template <int G>
+struct GroupSum {
+  static constexpr int kWarps = G / 32;
+  float2* slots;             // [2][kWarps] of this group
+  int flip, warp, bar;
+  __device__ __forceinline__ explicit GroupSum(float2* shared)   // [2 * kNormThreads / 32] of the block
+      : slots(shared + threadIdx.x / G * 2 * kWarps), flip(0), warp(threadIdx.x % G / 32), bar(1 + threadIdx.x / G) {}
+  template <bool kTwo>
+  __device__ __forceinline__ void sum(float& a, float& b) {
+    static_assert(G % 64 == 0, "two warps at least");
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      if (kTwo) b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    float2* s = slots + flip;
+    flip ^= kWarps;
+    if ((threadIdx.x & 31) == 0) s[warp] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(G) : "memory");
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; i += 2) {
+      const float4 t = *reinterpret_cast<const float4*>(s + i);
+      a += t.x;
+      a += t.z;
+      if (kTwo) b += t.y, b += t.w;
+    }
+  }
+  __device__ __forceinline__ void operator()(float& a) {
+    float unused = 0.f;
+    sum<false>(a, unused);
+  }
+  __device__ __forceinline__ void operator()(float& a, float& b) { sum<true>(a, b); }
+};
+constexpr int kSumSlots = 2 * kNormThreads / 32;
+
 template <typename T, int V, int P>
-__global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 sums[8 * 32];
+__global__ void __launch_bounds__(kNormThreads, 2) norm_forward_kernel(const __grid_constant__ NormParams p) {
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
-  GroupSum total = group_sum(sums, G);
   const float inv_n = 1.f / n;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
   float w[P * V], b[P * V];
@@ -165,7 +242,7 @@ __global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward
       load_f32<V>(p.bias, j, 0.f, b + k * V);
     }
   }
-  Raw<T, V> next[P];
+  Words<T, V> next[P];
   auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
 #pragma unroll
@@ -186,12 +263,11 @@ __global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward
 #pragma unroll
     for (int k = 0; k < P; ++k) next[k].to(v + k * V);
     fetch(row + step);
-    float mu = 0.f, unused = 0.f;
+    float mu = 0.f;
     if (p.mean) {
 #pragma unroll
       for (int i = 0; i < P * V; ++i) mu += v[i];
-      total(mu, unused);
-      mu *= inv_n;
+      mu = lane_sum(mu, G) * inv_n;
     }
     float q = 0.f;
 #pragma unroll
@@ -204,8 +280,7 @@ __global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward
         }
       }
     }
-    unused = 0.f;
-    total(q, unused);
+    q = lane_sum(q, G);
     const float rstd = 1.f / sqrtf(fmaf(q, inv_n, p.eps));
     if (row >= p.rows) continue;
     T* y = static_cast<T*>(p.out) + row * p.ldo;
@@ -216,7 +291,7 @@ __global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = fmaf(v[k * V + i] * rstd, w[k * V + i], b[k * V + i]);
-        store_pack<T, V>(y + j, o);
+        write_row<T, V>(y + j, o);
       }
     }
     if (t == 0) {
@@ -226,21 +301,51 @@ __global__ void __launch_bounds__(kNormThreads, V * P <= 8 ? 3 : 1) norm_forward
   }
 }
 
+// One partial row of dw and of db per block; `joined` is room for the columns
+// of its groups, [kNormThreads / G][n], where it has several.
+template <int V, int P>
+__device__ __forceinline__ void write_parts(const NormParams& p, int G, float* joined, int t, const float (&dw)[P * V],
+                                            const float (&db)[P * V]) {
+  const int n = p.n, per_block = kNormThreads / G;
+  for (int which = 0; which < 2; ++which) {
+    float* part = which ? p.part_b : p.part_w;
+    if (!part) continue;
+    part += static_cast<int64_t>(blockIdx.x) * n;
+    float* mine = part;
+    if (per_block > 1) {
+      __syncthreads();
+      mine = joined + static_cast<int64_t>(threadIdx.x / G) * n;
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int j = (k * G + t) * V;
+      if (j < n) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) mine[j + i] = which ? db[k * V + i] : dw[k * V + i];
+      }
+    }
+    if (per_block == 1) continue;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += kNormThreads) {
+      float s = 0.f;
+      for (int g = 0; g < per_block; ++g) s += joined[static_cast<int64_t>(g) * n + j];
+      part[j] = s;
+    }
+  }
+}
+
 // SUMS: also the partial rows of dw and db.
 template <typename T, int V, int P, bool SUMS>
-__global__ void __launch_bounds__(kNormThreads, SUMS ? 1 : 2) norm_backward_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 sums[8 * 32];
-  // [kNormThreads / G][n], where a block has several groups: at most kWide floats, 32 KB
-  extern __shared__ float joined[];
+__global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ float joined[];   // [kNormThreads / G][n]: at most kWide floats, 32 KB
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
-  GroupSum total = group_sum(sums, G);
   float dw[P * V], db[P * V];
 #pragma unroll
   for (int i = 0; i < P * V; ++i) dw[i] = db[i] = 0.f;
   const float inv_n = 1.f / n;
   const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
-  Raw<T, V> next_x[P], next_dy[P];
+  Words<T, V> next_x[P], next_dy[P];
   float next_mean = 0.f, next_rstd = 0.f;
   auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
@@ -291,7 +396,7 @@ __global__ void __launch_bounds__(kNormThreads, SUMS ? 1 : 2) norm_backward_kern
         }
       }
     }
-    total(sg, sgx);
+    lane_sum(sg, sgx, G);
     if (row >= p.rows) continue;
     const float mg = p.mean ? sg * inv_n : 0.f, mgx = sgx * inv_n;
     T* dx = static_cast<T*>(p.out) + row * p.ldo;
@@ -302,66 +407,272 @@ __global__ void __launch_bounds__(kNormThreads, SUMS ? 1 : 2) norm_backward_kern
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] = rstd * (g[k * V + i] - mg - v[k * V + i] * mgx);
-        store_pack<T, V>(dx + j, o);
+        write_row<T, V>(dx + j, o);
       }
     }
   }
-  // one partial row of dw and of db per block
-  for (int which = 0; which < (SUMS ? 2 : 0); ++which) {
-    float* part = which ? p.part_b : p.part_w;
-    if (!part) continue;
-    part += static_cast<int64_t>(blockIdx.x) * n;
-    if (per_block == 1) {
+  if constexpr (SUMS) write_parts<V, P>(p, G, joined, t, dw, db);
+}
+
+// ---- 128 or 512 threads per row: rows arrive in a ring in shared memory
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The ring of one group: `ring` slots of `kOperands` rows each.  Thread 0 of the
+// group fills slot i % ring with the group's i-th row, from the 16-byte piece
+// that the row starts in to the one that it ends in; a slot is filled again
+// once the group has passed a barrier after reading it.
+template <typename T, int kOperands, int G>
+struct RowRing {
+  uint8_t* base;
+  uint64_t* full;            // [ring]
+  int* err;
+  const T* src[kOperands];
+  int64_t ld[kOperands];
+  int ring, slot_bytes, n;
+  __device__ __forceinline__ void fill(int slot, int64_t row) {
+    uint32_t total = 0;
+    uintptr_t from[kOperands];
+    uint32_t bytes[kOperands];
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int j = (k * G + t) * V;
-        if (j < n) {
+    for (int o = 0; o < kOperands; ++o) {
+      const uintptr_t p = reinterpret_cast<uintptr_t>(src[o] + row * ld[o]);
+      from[o] = p & ~uintptr_t(15);
+      bytes[o] = static_cast<uint32_t>(((p + n * sizeof(T) + 15) & ~uintptr_t(15)) - from[o]);
+      total += bytes[o];
+    }
+    mbar_expect_tx(&full[slot], total);
 #pragma unroll
-          for (int i = 0; i < V; ++i) part[j + i] = which ? db[k * V + i] : dw[k * V + i];
+    for (int o = 0; o < kOperands; ++o)
+      bulk_load(base + (slot * kOperands + o) * slot_bytes, reinterpret_cast<const void*>(from[o]), bytes[o], &full[slot]);
+  }
+  // A wait that gives up records that and goes on: the group's barriers need all of its threads.
+  __device__ __forceinline__ void wait(int slot, uint32_t phase) { mbar_wait(&full[slot], phase, err); }
+  // After a wait that gave up, thread 0 of the group lets the copies of its last fills land (`next`: the row
+  // after the group's last one).
+  __device__ __forceinline__ void finish(int64_t next, int64_t first, int64_t step) {
+    if (*reinterpret_cast<volatile int*>(err) == 0) return;
+    const int64_t fills = (next - first) / step;
+    for (int64_t i = fills > ring ? fills - ring : 0; i < fills; ++i) {
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&full[i % ring], static_cast<uint32_t>(i / ring) & 1) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+    atomicOr(&g_norm_timeout, 1);
+  }
+  // the row in the slot, once it is there
+  __device__ __forceinline__ const T* at(int slot, int o, int64_t row) const {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(src[o] + row * ld[o]);
+    return reinterpret_cast<const T*>(base + (slot * kOperands + o) * slot_bytes + (p & 15));
+  }
+};
+
+// Per-block control words of the ring kernels, before the rows.
+struct RingShared {
+  alignas(16) float2 sums[kSumSlots];
+  uint64_t full[kNormThreads / 64 * kMaxRing];
+  int err;
+};
+constexpr int kRingOffset = (sizeof(RingShared) + 127) / 128 * 128;
+
+template <typename T, int kOperands, int G>
+__device__ __forceinline__ RowRing<T, kOperands, G> start_ring(const NormParams& p, uint8_t* smem, int64_t row, int64_t step) {
+  RingShared* sh = reinterpret_cast<RingShared*>(smem);
+  const int group = threadIdx.x / G;
+  RowRing<T, kOperands, G> r;
+  r.base = smem + kRingOffset + static_cast<size_t>(group) * p.ring * kOperands * p.slot;
+  r.full = sh->full + group * kMaxRing;
+  r.err = &sh->err;
+  r.src[0] = static_cast<const T*>(p.x);
+  r.ld[0] = p.ldx;
+  if constexpr (kOperands == 2) {
+    r.src[1] = static_cast<const T*>(p.dy);
+    r.ld[1] = p.lddy;
+  }
+  r.ring = p.ring;
+  r.slot_bytes = p.slot;
+  r.n = p.n;
+  if (threadIdx.x == 0) sh->err = 0;
+  if (threadIdx.x % G == 0) {
+    for (int s = 0; s < p.ring; ++s) mbar_init(&r.full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x % G == 0)
+    for (int s = 0; s < p.ring && row + s * step < p.rows; ++s) r.fill(s, row + s * step);
+  return r;
+}
+
+template <typename T, int V, int P, int G>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_forward_ring_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int per_block = kNormThreads / G;
+  const int t = threadIdx.x % G, n = p.n;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / G;
+  int64_t row = first;
+  GroupSum<G> total(reinterpret_cast<RingShared*>(smem)->sums);
+  RowRing<T, 1, G> ring = start_ring<T, 1, G>(p, smem, row, step);
+  const float inv_n = 1.f / n;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (; row < p.rows; row += step) {
+    ring.wait(slot, phase);
+    const T* x = ring.at(slot, 0, row);
+    float v[P * V];
+    float mu = 0.f, q = 0.f;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int j = (k * G + t) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k * V + i] = 0.f;
+      if (j < n) read_row<T, V>(x + j, v + k * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) mu += v[k * V + i];
+    }
+    // (the RMS norm needs this barrier too: the slot has been read after it)
+    total(mu);
+    mu = p.mean ? mu * inv_n : 0.f;
+    if (t == 0 && row + ring.ring * step < p.rows) ring.fill(slot, row + ring.ring * step);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if ((k * G + t) * V < n) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[k * V + i] -= mu;
+          q = fmaf(v[k * V + i], v[k * V + i], q);
         }
       }
-      continue;
     }
-    __syncthreads();
-    float* mine = joined + static_cast<int64_t>(threadIdx.x / G) * n;
+    total(q);
+    const float rstd = 1.f / sqrtf(fmaf(q, inv_n, p.eps));
+    T* y = static_cast<T*>(p.out) + row * p.ldo;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const int j = (k * G + t) * V;
       if (j < n) {
+        float w[V], b[V], o[V];
+        load_f32<V>(p.weight, j, 1.f, w);
+        load_f32<V>(p.bias, j, 0.f, b);
 #pragma unroll
-        for (int i = 0; i < V; ++i) mine[j + i] = which ? db[k * V + i] : dw[k * V + i];
+        for (int i = 0; i < V; ++i) o[i] = fmaf(v[k * V + i] * rstd, w[i], b[i]);
+        write_row<T, V>(y + j, o);
       }
     }
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kNormThreads) {
-      float s = 0.f;
-      for (int g = 0; g < per_block; ++g) s += joined[static_cast<int64_t>(g) * n + j];
-      part[j] = s;
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mu;
+      p.rstd[row] = rstd;
+    }
+    if (++slot == ring.ring) {
+      slot = 0;
+      phase ^= 1u;
     }
   }
+  if (t == 0) ring.finish(row, first, step);
+}
+
+template <typename T, int V, int P, int G, bool SUMS>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_backward_ring_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int per_block = kNormThreads / G;
+  const int t = threadIdx.x % G, n = p.n;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / G;
+  int64_t row = first;
+  GroupSum<G> total(reinterpret_cast<RingShared*>(smem)->sums);
+  RowRing<T, 2, G> ring = start_ring<T, 2, G>(p, smem, row, step);
+  float dw[P * V], db[P * V];
+#pragma unroll
+  for (int i = 0; i < P * V; ++i) dw[i] = db[i] = 0.f;
+  const float inv_n = 1.f / n;
+  int slot = 0;
+  uint32_t phase = 0;
+  float next_rstd = row < p.rows ? p.rstd[row] : 0.f;
+  float next_mean = row < p.rows && p.mean ? p.mean[row] : 0.f;
+  for (; row < p.rows; row += step) {
+    const float rstd = next_rstd, mu = next_mean;
+    if (row + step < p.rows) {
+      next_rstd = p.rstd[row + step];
+      if (p.mean) next_mean = p.mean[row + step];
+    }
+    ring.wait(slot, phase);
+    const T* x = ring.at(slot, 0, row);
+    const T* dy = ring.at(slot, 1, row);
+    float v[P * V], g[P * V];
+    float sg = 0.f, sgx = 0.f;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int j = (k * G + t) * V;
+#pragma unroll
+      for (int i = k * V; i < (k + 1) * V; ++i) v[i] = g[i] = 0.f;
+      if (j < n) {
+        float w[V];
+        read_row<T, V>(x + j, v + k * V);
+        read_row<T, V>(dy + j, g + k * V);
+        load_f32<V>(p.weight, j, 1.f, w);
+#pragma unroll
+        for (int i = k * V; i < (k + 1) * V; ++i) {
+          v[i] = (v[i] - mu) * rstd;
+          if (SUMS) {
+            dw[i] = fmaf(g[i], v[i], dw[i]);
+            db[i] += g[i];
+          }
+          g[i] *= w[i - k * V];
+          sg += g[i];
+          sgx = fmaf(g[i], v[i], sgx);
+        }
+      }
+    }
+    total(sg, sgx);
+    if (t == 0 && row + ring.ring * step < p.rows) ring.fill(slot, row + ring.ring * step);
+    const float mg = p.mean ? sg * inv_n : 0.f, mgx = sgx * inv_n;
+    T* dx = static_cast<T*>(p.out) + row * p.ldo;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int j = (k * G + t) * V;
+      if (j < n) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = rstd * (g[k * V + i] - mg - v[k * V + i] * mgx);
+        write_row<T, V>(dx + j, o);
+      }
+    }
+    if (++slot == ring.ring) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  if (t == 0) ring.finish(row, first, step);
+  __syncthreads();
+  // the ring's space is free: every copy has been waited for
+  if constexpr (SUMS) write_parts<V, P>(p, G, reinterpret_cast<float*>(smem + kRingOffset), t, dw, db);
 }
 
 // Rows wider than kWide: one block per row, three (two) walks over it.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_forward_wide_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 sums[8 * 32];
-  GroupSum total = group_sum(sums, kNormThreads);
+  __shared__ __align__(16) float2 sums[kSumSlots];
+  GroupSum<kNormThreads> total(sums);
   const float inv_n = 1.f / p.n;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     T* y = static_cast<T*>(p.out) + row * p.ldo;
-    float mu = 0.f, s = 0.f, unused = 0.f, q = 0.f;
+    float mu = 0.f, s = 0.f, q = 0.f;
     if (p.mean) {
       for (int j = threadIdx.x; j < p.n; j += kNormThreads) s += to_f(x[j]);
-      total(s, unused);
+      total(s);
       mu = s * inv_n;
     }
     for (int j = threadIdx.x; j < p.n; j += kNormThreads) {
       const float d = to_f(x[j]) - mu;
       q = fmaf(d, d, q);
     }
-    unused = 0.f;
-    total(q, unused);
+    total(q);
     const float rstd = 1.f / sqrtf(fmaf(q, inv_n, p.eps));
     for (int j = threadIdx.x; j < p.n; j += kNormThreads)
       y[j] = from_f<T>(fmaf((to_f(x[j]) - mu) * rstd, p.weight ? p.weight[j] : 1.f, p.bias ? p.bias[j] : 0.f));
@@ -374,8 +685,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_wide_kernel(const _
 
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float2 sums[8 * 32];
-  GroupSum total = group_sum(sums, kNormThreads);
+  __shared__ __align__(16) float2 sums[kSumSlots];
+  GroupSum<kNormThreads> total(sums);
   const float inv_n = 1.f / p.n;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
@@ -460,6 +771,11 @@ bool packed(const void* p, int64_t ld, int64_t n, int size) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * size) % 16 == 0 && (n * size) % 16 == 0;
 }
 
+// Packs of 4 elements: the same for 4 elements' alignment.
+bool fours(const void* p, int64_t ld, int64_t n, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & (4 * size - 1)) == 0 && ld % 4 == 0 && n % 4 == 0;
+}
+
 // Threads per row: the fewest (a power of two) that hold the row with `most`
 // elements each.
 int group_for(int64_t n, int most) {
@@ -474,26 +790,50 @@ enum Pass { kForward, kBackward, kBackwardRows };   // kBackwardRows: dx alone
 
 template <typename T, int V, int P>
 cudaError_t launch_row(const NormParams& p, Pass pass, int grid, size_t smem, cudaStream_t s) {
-  if (pass == kForward)
-    norm_forward_kernel<T, V, P><<<grid, kNormThreads, 0, s>>>(p);
-  else if (pass == kBackward)
+  if (pass == kForward) {
+    if constexpr (V * P <= 8) norm_forward_kernel<T, V, P><<<grid, kNormThreads, 0, s>>>(p);   // at most 8 elements
+  } else if (pass == kBackward)
     norm_backward_kernel<T, V, P, true><<<grid, kNormThreads, smem, s>>>(p);
   else
     norm_backward_kernel<T, V, P, false><<<grid, kNormThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
+template <typename T, int V, int P, int G>
+cudaError_t launch_ring(const NormParams& p, Pass pass, int grid, size_t smem, cudaStream_t s) {
+  void (*kernel)(NormParams) = pass == kForward    ? norm_forward_ring_kernel<T, V, P, G>
+                               : pass == kBackward ? norm_backward_ring_kernel<T, V, P, G, true>
+                                                   : norm_backward_ring_kernel<T, V, P, G, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kNormThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// 128 or 512 threads per row, with 8 or 16 elements each.  The group's size is
+// a constant of the kernel: with addresses computed from a size at run time, the
+// kernels were bound by their instructions (37 per element).
+int ring_group(int64_t n) { return n <= 128 * kMaxPack ? 128 : 512; }
+template <typename T, int V>
+cudaError_t launch_rings(const NormParams& p, Pass pass, int grid, size_t smem, cudaStream_t s) {
+  if (p.group == 128)
+    return p.n <= 128 * 8 ? launch_ring<T, V, 8 / V, 128>(p, pass, grid, smem, s)
+                          : launch_ring<T, V, 16 / V, 128>(p, pass, grid, smem, s);
+  return p.n <= 512 * 8 ? launch_ring<T, V, 8 / V, 512>(p, pass, grid, smem, s)
+                        : launch_ring<T, V, 16 / V, 512>(p, pass, grid, smem, s);
+}
+
+// vec: packs of 16 bytes (rows of up to 32 lanes) or of 4 elements (the ring).
 template <typename T>
-cudaError_t launch_typed(NormParams p, Pass pass, bool vec, int elems, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_typed(const NormParams& p, Pass pass, bool vec, int elems, int grid, size_t smem, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
+  if (p.group > 32) return vec ? launch_rings<T, 4>(p, pass, grid, smem, s) : launch_rings<T, 1>(p, pass, grid, smem, s);
   if (vec) {
     if (elems <= V) return launch_row<T, V, 1>(p, pass, grid, smem, s);
     if (elems <= 8) return launch_row<T, V, 8 / V>(p, pass, grid, smem, s);
-    return launch_row<T, V, 16 / V>(p, pass, grid, smem, s);
+    if constexpr (V == 8) return launch_row<T, 8, 2>(p, pass, grid, smem, s);
   }
-  if (elems <= 4) return launch_row<T, 1, 4>(p, pass, grid, smem, s);
-  if (elems <= 8) return launch_row<T, 1, 8>(p, pass, grid, smem, s);
-  return launch_row<T, 1, 16>(p, pass, grid, smem, s);
+  return launch_row<T, 1, 8>(p, pass, grid, smem, s);
 }
 
 cudaError_t launch(const NormParams& p, int32_t dtype, Pass pass, bool vec, int elems, int grid, size_t smem,
@@ -501,6 +841,17 @@ cudaError_t launch(const NormParams& p, int32_t dtype, Pass pass, bool vec, int 
   if (dtype == MUONH_DTYPE_F32) return launch_typed<float>(p, pass, vec, elems, grid, smem, s);
   if (dtype == MUONH_DTYPE_BF16) return launch_typed<__nv_bfloat16>(p, pass, vec, elems, grid, smem, s);
   return launch_typed<__half>(p, pass, vec, elems, grid, smem, s);
+}
+
+// Sizes p's ring; returns the dynamic shared memory.  `budget` bytes per block;
+// two rows at least.
+size_t size_ring(NormParams* p, int operands, int size, size_t budget) {
+  const size_t groups = kNormThreads / p->group;
+  p->slot = static_cast<int32_t>((static_cast<size_t>(p->n) * size + 15) / 16 * 16 + 16);
+  p->ring = static_cast<int32_t>(std::max<size_t>(2, std::min<size_t>(kMaxRing, budget / (groups * operands * p->slot))));
+  const size_t rows = groups * p->ring * operands * p->slot;
+  const size_t joined = groups > 1 && operands == 2 ? groups * p->n * sizeof(float) : 0;
+  return kRingOffset + std::max(rows, joined);
 }
 
 // Partial rows of dw and db from x and dy: a thread per column, `slices` shares of the rows.
@@ -573,13 +924,21 @@ extern "C" muonh_status muonh_layer_norm(const void* x, int64_t ldx, void* y, in
         : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, kForward, grid, s)
                                     : launch_wide<__half>(p, kForward, grid, s);
   } else {
-    const bool vec = packed(x, ldx, n, size) && packed(y, ldy, n, size) && aligned16(weight) && aligned16(bias);
-    // 8 elements per thread leave room for three blocks per SM
-    p.group = group_for(n, n <= kNormThreads * 8 ? 8 : kMaxPack);
+    // 8 elements per thread of rows within a warp, 16 beyond: both leave room for two blocks per SM
+    p.group = group_for(n, 8);
+    size_t smem = 0;
+    bool vec;
+    if (p.group > 32) {
+      p.group = ring_group(n);
+      vec = fours(x, ldx, n, size) && fours(y, ldy, n, size) && aligned16(weight) && aligned16(bias);
+      smem = size_ring(&p, 1, size, 100 * 1024);
+    } else {
+      vec = packed(x, ldx, n, size) && packed(y, ldy, n, size) && aligned16(weight) && aligned16(bias);
+    }
     const int elems = static_cast<int>((n + p.group - 1) / p.group);
     const int64_t blocks = (rows + kNormThreads / p.group - 1) / (kNormThreads / p.group);
-    const int grid = static_cast<int>(std::min<int64_t>(blocks, (elems <= 8 ? 3ll : 1ll) * sm_count()));   // all at once
-    e = launch(p, dtype, kForward, vec, elems, grid, 0, s);
+    const int grid = static_cast<int>(std::min<int64_t>(blocks, 2ll * sm_count()));   // all at once
+    e = launch(p, dtype, kForward, vec, elems, grid, smem, s);
   }
   if (e != cudaSuccess) return norm_fail(MUONH_ERR_CUDA, "launch of the layer norm kernel failed");
   return MUONH_OK;
@@ -633,13 +992,6 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
   int parts;
   cudaError_t e;
   float* part = static_cast<float*>(workspace);
-  const bool vec = packed(x, ldx, n, size) && packed(dy, lddy, n, size) && packed(dx, lddx, n, size) &&
-                   aligned16(weight);
-  // the column sums of 16 elements per thread fit next to a prefetched row
-  // only where both rows are packed 16-bit; else they come from a kernel of
-  // their own (x and dy are then read twice, the second time mostly from L2)
-  const int most = vec && size == 2 ? kMaxPack : 8;
-  const bool split = sums && n > static_cast<int64_t>(kNormThreads) * most;
   auto set_parts = [&](int count) {   // a single partial row is the result
     parts = count;
     if (dweight) p.part_w = parts == 1 ? dweight : part;
@@ -651,23 +1003,29 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
     e = dtype == MUONH_DTYPE_F32    ? launch_wide<float>(p, kBackward, grid, s)
         : dtype == MUONH_DTYPE_BF16 ? launch_wide<__nv_bfloat16>(p, kBackward, grid, s)
                                     : launch_wide<__half>(p, kBackward, grid, s);
+    if (e == cudaSuccess && sums) {
+      set_parts(static_cast<int>(std::min<int64_t>(rows, 64)));
+      e = launch_columns(p, dtype, parts, s);
+    }
   } else {
-    p.group = group_for(n, split || !sums ? kMaxPack : most);
+    // rows within a warp: 16 packed 16-bit elements per thread fit in the
+    // registers next to the column sums and the next row, 8 of the others
+    bool vec = packed(x, ldx, n, size) && packed(dy, lddy, n, size) && packed(dx, lddx, n, size) && aligned16(weight);
+    p.group = group_for(n, vec && size == 2 ? kMaxPack : 8);
+    size_t smem = 0;
+    if (p.group > 32) {
+      p.group = ring_group(n);
+      vec = fours(x, ldx, n, size) && fours(dy, lddy, n, size) && fours(dx, lddx, n, size) && aligned16(weight);
+      smem = size_ring(&p, 2, size, 200 * 1024);
+    } else if (sums && p.group < kNormThreads) {
+      smem = static_cast<size_t>(kNormThreads / p.group) * n * sizeof(float);
+    }
     const int elems = static_cast<int>((n + p.group - 1) / p.group);
     const int per_block = kNormThreads / p.group;
-    const int64_t blocks = (rows + per_block - 1) / per_block;
-    if (split || !sums) {
-      e = launch(p, dtype, kBackwardRows, vec, elems, static_cast<int>(std::min<int64_t>(blocks, 2ll * sms)), 0, s);
-    } else {
-      const int grid = static_cast<int>(std::min<int64_t>({blocks, sms, static_cast<int64_t>(kMaxParts)}));
-      set_parts(grid);
-      const size_t smem = per_block > 1 ? static_cast<size_t>(per_block) * n * sizeof(float) : 0;
-      e = launch(p, dtype, kBackward, vec, elems, grid, smem, s);
-    }
-  }
-  if (e == cudaSuccess && split) {
-    set_parts(static_cast<int>(std::min<int64_t>(rows, 64)));
-    e = launch_columns(p, dtype, parts, s);
+    const int grid = static_cast<int>(
+        std::min<int64_t>({(rows + per_block - 1) / per_block, sms, static_cast<int64_t>(kMaxParts)}));
+    if (sums) set_parts(grid);
+    e = launch(p, dtype, sums ? kBackward : kBackwardRows, vec, elems, grid, smem, s);
   }
   if (e == cudaSuccess && sums && parts > 1) {
     norm_join_kernel<<<dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1), 32 * kJoinSlices, 0, s>>>(
@@ -677,3 +1035,5 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
   if (e != cudaSuccess) return norm_fail(MUONH_ERR_CUDA, "launch of a layer norm backward kernel failed");
   return MUONH_OK;
 }
+
+cudaError_t muonh::take_norm_timeout(int* flag, cudaStream_t s) { return take_flag(g_norm_timeout, flag, s); }

@@ -763,11 +763,4 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   return MUONH_OK;
 }
 
-cudaError_t muonh::take_orth_timeout(int* flag, cudaStream_t s) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_orth_timeout, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && *flag) e = cudaMemcpyToSymbolAsync(g_orth_timeout, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return e;
-}
+cudaError_t muonh::take_orth_timeout(int* flag, cudaStream_t s) { return take_flag(g_orth_timeout, flag, s); }
