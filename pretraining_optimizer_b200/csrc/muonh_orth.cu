@@ -22,6 +22,10 @@
 // rank order, and every CTA then runs the same r x r iteration: with few
 // matrices the SMs would otherwise be idle, with many the cluster is one CTA.
 //
+// What bounds it.  The r x r iteration is a chain of 14 dependent products of 24
+// MMAs (128 x 128 x 16) with a pass of the epilogue between them: 55 of the 70 us
+// a lone matrix [128, 2048] takes at 8 CTAs... see kLateNs for many of them.
+//
 // Precision.  The products are 16-bit with fp32 accumulation.  X X^T is exact
 // up to the accumulation: X is used as it is.  The r x r operands are kept as
 // fp16 pairs (hi + lo, 22 bits) and each product is hi hi + hi lo + lo hi:
@@ -50,10 +54,16 @@ constexpr int kBarsOffset = kQOffset + kPairBytes;
 constexpr int kOrthSmem = kBarsOffset + 1024 + 1024;   // barriers, scalars; alignment slack
 static_assert(kRing * kSliceBytes == 2 * kPairBytes, "A and P share the ring's space");
 static_assert(kOrthSmem <= 227 * 1024, "shared memory of the orthogonalize kernel exceeds 227 KB");
-constexpr int kEpiThreads = 256;                  // 8 epilogue warps
+constexpr int kEpiThreads = 512;                  // 16 epilogue warps: 32 rows x 32 columns each
 constexpr int kOrthThreads = 64 + kEpiThreads;    // warp 0 TMA, warp 1 MMA
 constexpr int kGramChunk = 16;                    // slices (2048 columns) per TMEM accumulation
 constexpr int kMaxSteps = 16;
+// With several matrices per SM all SMs read X, iterate and write at the same
+// time, and HBM idles during the r x r iterations.  Half of the SMs start a
+// quarter of a matrix later: 896 x [128, 2048] took 470 us without, 436 with 15
+// us, 441 with 35 us; below four matrices per SM the delay costs what it gives.
+constexpr int kLateNs = 15000;
+constexpr int kLateWaves = 4;
 constexpr int kMaxCluster = 8;
 
 __device__ int g_orth_timeout;                    // a wait gave up in some call since the flag was read
@@ -67,6 +77,8 @@ struct OrthParams {
   // step k; and the final Q
   int32_t ea, eb, eq[kMaxSteps], eq_last;
   int32_t rows, cols;        // of X, for skipping stores outside
+  int32_t late_below;        // odd CTAs below this number start kLateNs late
+  int32_t used;              // small side rounded up to 64 or 128: columns and k of the r x r products
 };
 
 __device__ __forceinline__ uint32_t row_piece(int row, int piece) {
@@ -87,6 +99,34 @@ template <bool BF16>
 __device__ __forceinline__ float2 unpack_16(uint32_t u) {
   if (!BF16) return __half22float2(*reinterpret_cast<__half2*>(&u));
   return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u));
+}
+
+// TMA with an L2 eviction priority: X is read a second time and is to stay until
+// then, what is read last or written goes first.
+__device__ __forceinline__ uint64_t policy_keep() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_drop() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const void* src, int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
 }
 
 // 32 values of one row as a 16-bit pair hi + lo: pieces piece0 .. piece0 + 3
@@ -111,19 +151,35 @@ __device__ __forceinline__ void store_split(uint8_t* hi, int row, int piece0, co
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// D (+)= L R for the 128 x 128 pairs at l and r: L K-major, R MN-major, both
-// as their rows are stored.  R is symmetric up to rounding, but reading it as
-// its transpose (K-major) compounds that asymmetry from product to product: the
-// last A_k was off by 1e-4 instead of 1e-6.
-__device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r, uint32_t idesc) {
-  for (int prod = 0; prod < 3; ++prod) {          // hi hi, hi lo, lo hi
-    const uint32_t lo_l = l + (prod == 2 ? kSliceBytes : 0), lo_r = r + (prod == 1 ? kSliceBytes : 0);
+// Descriptors of a 128 x 128 slice or operand (two chunks of 128 rows x 64
+// columns), and their advance over k steps of 16 along k.
+__device__ __forceinline__ uint64_t k_major(uint32_t at) { return sdesc_sw128(at, 16, 1024); }
+__device__ __forceinline__ uint64_t mn_major(uint32_t at) { return sdesc_sw128(at, kChunkBytes, 1024); }
+__device__ constexpr uint32_t k_major_step(int k) { return ((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4; }
+__device__ constexpr uint32_t mn_major_step(int k) { return (k * 16 * 128) >> 4; }
+
+// D (+)= L R over K steps: L K-major, R MN-major, both as their rows are
+// stored.  Inlined straight-line code, so that the descriptors are computed in
+// uniform registers: in a function of its own, in a loop, or with a branch around
+// each MMA, one took 135 cycles to issue, against the 64 to 81 that it takes to
+// run.  The small side is rounded up to 64 or 128 for that (kHalf, kFull).
+constexpr int kHalf = 4, kFull = 8;
+template <int K>
+__device__ __forceinline__ void products(uint32_t d, uint64_t left, uint64_t right, uint32_t idesc, uint32_t accumulate) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      umma_f16(d, sdesc_sw128(lo_l + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
-               sdesc_sw128(lo_r + k * 2048, kChunkBytes, 1024), idesc, (prod | k) != 0);
-    }
-  }
+  for (int k = 0; k < K; ++k)
+    umma_f16(d, left + k_major_step(k), right + mn_major_step(k), idesc, k == 0 ? accumulate : 1u);
+}
+
+// D = L R for the 128 x 128 pairs at l and r: hi hi + hi lo + lo hi.  R is
+// symmetric up to rounding, but reading it as its transpose (K-major) compounds
+// that asymmetry from product to product: the last A_k was off by 1e-4 instead
+// of 1e-6.
+template <int K>
+__device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r, uint32_t idesc) {
+#pragma unroll 1
+  for (int prod = 0; prod < 3; ++prod)
+    products<K>(d, k_major(l + (prod == 2 ? kSliceBytes : 0)), mn_major(r + (prod == 1 ? kSliceBytes : 0)), idesc, prod);
 }
 
 // 16 bytes of another CTA's shared memory (the callers' cluster barriers order it).
@@ -135,20 +191,20 @@ __device__ __forceinline__ float4 load_cluster(uint32_t addr) {
   return v;
 }
 
-// The sum over the cluster's R CTAs of the 64 values of each epilogue thread,
-// which every CTA has left at smem as 16 vectors per thread.  Each CTA adds
-// 16/R of the vectors, in rank order, and then all fetch each other's: 2 x 64
+// The sum over the cluster's R CTAs of the 32 values of each epilogue thread,
+// which every CTA has left at smem as 8 vectors per thread.  Each CTA adds
+// 8/R of the vectors, in rank order, and then all fetch each other's: 2 x 64
 // KB per CTA instead of R x 64 KB, and the same sums everywhere.  Loads start
 // at the next CTA, so that no CTA's shared memory is read by all at once.
 // All threads call it, between two cluster barriers.
 template <int R>
-__device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (&acc)[64]) {
-  constexpr int kEach = 16 / R;
+__device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (&acc)[32]) {
+  constexpr int kEach = 8 / R;
   const bool mine = threadIdx.x >= 64;
   const uint32_t at = (threadIdx.x - 64) * 16;
   float4* const own = reinterpret_cast<float4*>(smem) + (threadIdx.x - 64);
   if (mine) {
-    float4 v[16];
+    float4 v[8];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const uint32_t from = map_shared_rank(smem, (rank + 1 + i) % R) + at;
@@ -196,7 +252,7 @@ __device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (
   }
 }
 
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 template <bool BF16>
 __global__ void __launch_bounds__(kOrthThreads, 1)
@@ -218,7 +274,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   uint64_t* drain = done_q + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
-  float* trace = reinterpret_cast<float*>(err + 1);   // [8]: the epilogue warps' shares
+  float* trace = reinterpret_cast<float*>(err + 1);   // [4]: shares of the diagonal
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t ranks;
@@ -229,12 +285,16 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const int count = static_cast<int>(static_cast<int64_t>(p.slices) * (rank + 1) / ranks) - first;
   const int chunks = (count + kGramChunk - 1) / kGramChunk;
 
+  if (static_cast<int>(blockIdx.x) < p.late_below && (blockIdx.x & 1)) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < kLateNs) __nanosleep(500);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&full[kRing + s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&empty[kRing + s], kEpiThreads / 32);
+      mbar_init(&empty[kRing + s], kEpiThreads / 64);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&tfull[i], 1);
@@ -261,6 +321,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   auto produce = [&](int pass) {
     uint64_t* f = full + pass * kRing;
     uint64_t* e = empty + pass * kRing;
+    const uint64_t policy = pass == 0 ? policy_keep() : policy_drop();
     int i = 0;
     for (; i < count; ++i) {
       const int slot = i % kRing;
@@ -269,7 +330,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       uint8_t* dst = smem + slot * kSliceBytes;
       const int at = (first + i) * kSide;
       for (int h = 0; h < 2; ++h)
-        tma_load_3d(dst + h * kChunkBytes, &xmap, &f[slot], p.tall ? 64 * h : at + 64 * h, p.tall ? at : 0, matrix);
+        load_box(dst + h * kChunkBytes, &xmap, &f[slot], p.tall ? 64 * h : at + 64 * h, p.tall ? at : 0, matrix,
+                 policy);
     }
     for (int j = i > kRing ? i - kRing : 0; j < i; ++j) {
       const uint64_t t0 = globaltimer();
@@ -278,13 +340,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     }
   };
 
-  // epilogue threads: one row and 64 of its columns each (a warp reaches the
+  // epilogue threads: one row and 32 of its columns each (a warp reaches the
   // TMEM lanes of its number mod 4)
-  const int quarter = warp & 3, half = (warp - 2) >> 2;
-  const int row = quarter * 32 + lane, col0 = half * 64;
+  const int quarter = warp & 3, col0 = ((warp - 2) >> 2) * 32;
+  const int row = quarter * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  const int ch = half * kChunkBytes;               // this thread's 64-column chunk
-  float acc[64];                                   // its part of X X^T, then of A_k
+  const int ch = (col0 >> 6) * kChunkBytes;        // the 64-column chunk of these columns
+  const int piece0 = (col0 & 32) >> 3;             // and their first 16-byte piece in its rows
+  const bool inside = col0 < p.used;               // columns behind the small side are not computed (per warp)
+  float acc[32];                                   // its part of X X^T, then of A_k
 
   // ------------------------------------------------------------ X X^T
   if (warp == 0) {
@@ -292,7 +356,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f16(kSide, kSide, BF16, p.tall) | (static_cast<uint32_t>(p.tall) << 15);
+      const uint32_t idesc = idesc_f16(kSide, p.used, BF16, p.tall) | (static_cast<uint32_t>(p.tall) << 15);
       bool ok = true;
       for (int i = 0; i < count && ok; ++i) {
         const int slot = i % kRing, chunk = i / kGramChunk;
@@ -301,11 +365,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+        const uint64_t d = p.tall ? mn_major(x) : k_major(x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint64_t d = p.tall ? sdesc_sw128(x + k * 2048, kChunkBytes, 1024)
-                                    : sdesc_sw128(x + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
-          umma_f16(tmem + (chunk & 1) * kSide, d, d, idesc, (i % kGramChunk) != 0 || k != 0);
+          const uint64_t dk = d + (p.tall ? mn_major_step(k) : k_major_step(k));
+          umma_f16(tmem + (chunk & 1) * kSide, dk, dk, idesc, (i % kGramChunk) != 0 || k != 0);
         }
         umma_commit(&empty[slot]);
         if (i % kGramChunk == kGramChunk - 1 || i == count - 1) umma_commit(&tfull[chunk & 1]);
@@ -314,16 +378,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     __syncwarp();
   } else {
 #pragma unroll
-    for (int j = 0; j < 64; ++j) acc[j] = 0.f;
+    for (int j = 0; j < 32; ++j) acc[j] = 0.f;
     for (int c = 0; c < chunks; ++c) {
       if (!mbar_wait(&tfull[c & 1], (c >> 1) & 1, err)) break;
       tc_fence_after();
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      if (inside) {
         float v[32];
-        tmem_ld32(tmem + lanes + (c & 1) * kSide + col0 + 32 * g, v);
+        tmem_ld32(tmem + lanes + (c & 1) * kSide + col0, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[32 * g + j] += v[j];
+        for (int j = 0; j < 32; ++j) acc[j] += v[j];
       }
       tc_fence_before();
       mbar_arrive(&tempty[c & 1]);
@@ -331,7 +394,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (ranks > 1) {   // this CTA's share, for the others to add
       float4* mine = reinterpret_cast<float4*>(smem) + (threadIdx.x - 64);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int j = 0; j < 8; ++j)
         mine[j * kEpiThreads] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
     }
   }
@@ -350,72 +413,55 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   float scale = 0.f;                                // 1 / (||X|| + eps)
   if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f16(kSide, kSide, 0, 1);
-      const uint32_t a = smem_u32(sm_a), pp = smem_u32(sm_p), q = smem_u32(sm_q);
+      const uint32_t idesc = idesc_f16(kSide, p.used, 0, 1);
+      const uint32_t a = smem_u32(sm_a), q = smem_u32(sm_q);
+      // per step: A_k^2 once A_k is there, A_k P_k once P_k is, (A_k P_k) P_k once A_k P_k is, and then
+      // Q_k P_k, which runs while the epilogue works on A_{k+1}.  The last step has the first and the Q
+      // product only, the first step no Q product (P_0 is Q_1).
       int waits = 0;
-      auto wait_ready = [&] {
-        const bool ok = mbar_wait(ready, waits++ & 1, err);
-        tc_fence_after();
-        return ok;
-      };
-      for (int k = 0; k < p.steps; ++k) {
-        if (!wait_ready()) break;                   // A_k
-        pair_product(tm_d, a, a, idesc);
-        umma_commit(done);
-        if (!wait_ready()) break;                   // P_k
-        if (k < p.steps - 1) {
-          pair_product(tm_d, a, pp, idesc);
-          umma_commit(done);
+      bool ok = true;
+      for (int n = 0; n < 4 * p.steps && ok; ++n) {
+        const int k = n >> 2, phase = n & 3;
+        const bool last = k == p.steps - 1;
+        if (phase < 2 || (phase == 2 && !last)) {    // the last P_k has to be there for its Q product, too
+          ok = mbar_wait(ready, waits++ & 1, err);
+          tc_fence_after();
         }
-        if (k > 0) {
-          pair_product(tm_q, q, pp, idesc);
-          umma_commit(done_q);
-        }
-        if (k < p.steps - 1) {
-          if (!wait_ready()) break;                 // A_k P_k
-          pair_product(tm_d, a, pp, idesc);
-          umma_commit(done);
-        }
+        if (!ok || (last && (phase == 1 || phase == 2)) || (k == 0 && phase == 3)) continue;
+        const uint32_t pk = k == 0 ? q : smem_u32(sm_p);
+        const uint32_t d = phase == 3 ? tm_q : tm_d, l = phase == 3 ? q : a, r = phase == 0 ? a : pk;
+        if (p.used == 64)
+          pair_product<kHalf>(d, l, r, idesc);
+        else
+          pair_product<kFull>(d, l, r, idesc);
+        umma_commit(phase == 3 ? done_q : done);
       }
     }
     __syncwarp();
   } else if (warp >= 2) {
-    // ||X||^2 is the trace; summed over a warp's rows, then over the warps in turn
+    // ||X||^2 is the trace; summed over a warp's rows, then over the warps
+    const bool diagonal = col0 == quarter * 32;     // this warp's block holds diagonal elements, one per lane
     float d = 0.f;
+    if (diagonal) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-      if (col0 + j == row) d = acc[j];
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) trace[warp - 2] = d;
+      for (int j = 0; j < 32; ++j)
+        if (j == lane) d = acc[j];
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) trace[quarter] = d;
+    }
     epilogue_sync();
-    d = 0.f;
-    for (int i = 0; i < 8; ++i) d += trace[i];
+    d = (trace[0] + trace[1]) + (trace[2] + trace[3]);
     const float norm = sqrtf(d) + p.eps;
     scale = norm > 0.f ? 1.f / norm : (norm == 0.f ? 0.f : norm);   // zeros stay zeros, NaN stays NaN
+    // from here on acc is 2^ea A_k
+    const float start = scale * exp2i(p.ea);
 #pragma unroll
-    for (int j = 0; j < 64; ++j) acc[j] = acc[j] * scale * scale;
+    for (int j = 0; j < 32; ++j) acc[j] = acc[j] * scale * start;
 
     auto publish = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(bar);
-    };
-    // the thread's 64 values of an r x r operand, f(j) of column col0 + j, times 2^e
-    auto write_f16 = [&](uint8_t* to, auto f) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float v[32];
-        f(g, v);
-        store_split<false>(to + ch, row, 4 * g, v);
-      }
-    };
-    auto write_q = [&](auto f) {                    // the final Q, in X's type
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float v[32];
-        f(g, v);
-        store_split<BF16>(sm_q + ch, row, 4 * g, v);
-      }
     };
     int n_done = 0, n_done_q = 0;
     auto wait_done = [&] {
@@ -423,74 +469,79 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       tc_fence_after();
       return ok;
     };
-    auto wait_done_q = [&] {
-      const bool ok = mbar_wait(done_q, n_done_q++ & 1, err);
-      tc_fence_after();
-      return ok;
-    };
     const float f_last = exp2i(p.eq_last);
+    float v[32];
+    auto read_scaled = [&](uint32_t from, float f) {
+      tmem_ld32(from + lanes + col0, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= f;
+    };
+    auto add_diagonal = [&](float x) {
+      if (!diagonal) return;
+      const uint32_t mine = 1u << lane;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (mine & (1u << j)) v[j] += x;
+    };
     bool ok = true;
-    if (p.steps == 0)
-      write_q([&](int g, float (&v)[32]) {
+    if (p.steps == 0 && inside) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = row == col0 + 32 * g + j ? f_last : 0.f;
-      });
-    for (int k = 0; k < p.steps && ok; ++k) {
+      for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      add_diagonal(f_last);
+      store_split<BF16>(sm_q + ch, row, piece0, v);
+    }
+    for (int k = 0; k < p.steps; ++k) {
       const bool last = k == p.steps - 1;
-      const float fa = exp2i(p.ea);
-      write_f16(sm_a, [&](int g, float (&v)[32]) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = acc[32 * g + j] * fa;
-      });
+      const int ep = k == 0 ? p.eq[0] : p.eb;       // P_0 is Q_1 and is stored as such
+      if (inside) store_split<false>(sm_a + ch, row, piece0, acc);
       publish(ready);
+      if (k > 1) {
+        // Q_{k-1} P_{k-1} from the step before, while A_k^2 runs
+        ok = mbar_wait(done_q, n_done_q++ & 1, err);
+        tc_fence_after();
+        if (!ok) break;
+        if (inside) {
+          read_scaled(tm_q, exp2i(p.eq[k - 1] - p.eq[k - 2] - p.eb));
+          store_split<false>(sm_q + ch, row, piece0, v);
+        }
+      }
       // P = a I + b A + c A^2
       if (!(ok = wait_done())) break;
-      const float fc = p.c * exp2i(-2 * p.ea), fp = exp2i(p.eb);
-      auto poly = [&](int g, float f, float (&v)[32]) {
-        tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
+      if (inside) {
+        const float f = (last && k == 0) ? f_last : exp2i(ep);
+        const float fc = p.c * f * exp2i(-2 * p.ea), fb = p.b * f * exp2i(-p.ea);
+        tmem_ld32(tm_d + lanes + col0, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float diag = row == col0 + 32 * g + j ? p.a : 0.f;
-          v[j] = fmaf(fc, v[j], fmaf(p.b, acc[32 * g + j], diag)) * f;
-        }
-      };
-      if (!(last && k == 0)) write_f16(sm_p, [&](int g, float (&v)[32]) { poly(g, fp, v); });
-      if (k == 0 && !last) write_f16(sm_q, [&](int g, float (&v)[32]) { poly(g, exp2i(p.eq[0]), v); });
-      if (k == 0 && last) write_q([&](int g, float (&v)[32]) { poly(g, f_last, v); });
-      publish(ready);
-      if (!last) {
-        // A P replaces A
-        if (!(ok = wait_done())) break;
-        const float ft = exp2i(-p.eb);
-        write_f16(sm_a, [&](int g, float (&v)[32]) {
-          tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= ft;
-        });
-        publish(ready);
-      }
-      if (k > 0) {
-        if (!(ok = wait_done_q())) break;
-        auto product = [&](int g, float f, float (&v)[32]) {
-          tmem_ld32(tm_q + lanes + col0 + 32 * g, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= f;
-        };
-        if (last)
-          write_q([&](int g, float (&v)[32]) { product(g, exp2i(p.eq_last - p.eq[k - 1] - p.eb), v); });
+        for (int j = 0; j < 32; ++j) v[j] = fmaf(fc, v[j], fb * acc[j]);
+        add_diagonal(p.a * f);
+        if (last && k == 0)
+          store_split<BF16>(sm_q + ch, row, piece0, v);
         else
-          write_f16(sm_q, [&](int g, float (&v)[32]) { product(g, exp2i(p.eq[k] - p.eq[k - 1] - p.eb), v); });
+          store_split<false>((k == 0 ? sm_q : sm_p) + ch, row, piece0, v);
       }
-      if (!last) {
-        if (!(ok = wait_done())) break;
-        const float fn = exp2i(-p.ea - p.eb);
+      publish(ready);
+      if (last) break;
+      // A P replaces A
+      if (!(ok = wait_done())) break;
+      if (inside) {
+        read_scaled(tm_d, exp2i(-ep));
+        store_split<false>(sm_a + ch, row, piece0, v);
+      }
+      publish(ready);
+      if (!(ok = wait_done())) break;
+      if (inside) {
+        tmem_ld32(tm_d + lanes + col0, acc);
+        const float fn = exp2i(-ep);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float v[32];
-          tmem_ld32(tm_d + lanes + col0 + 32 * g, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[32 * g + j] = v[j] * fn;
-        }
+        for (int j = 0; j < 32; ++j) acc[j] *= fn;
+      }
+    }
+    if (ok && p.steps > 1) {                        // the final Q, in X's type
+      ok = mbar_wait(done_q, n_done_q++ & 1, err);
+      tc_fence_after();
+      if (inside) {
+        read_scaled(tm_q, exp2i(p.eq_last - p.eq[p.steps - 2] - p.eb));
+        store_split<BF16>(sm_q + ch, row, piece0, v);
       }
     }
     publish(q_ready);
@@ -503,7 +554,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f16(kSide, kSide, BF16, 1);
+      // wide: N is the slice's width and k the small side; tall: N and k are the small side
+      const uint32_t idesc = idesc_f16(kSide, p.tall ? p.used : kSide, BF16, 1);
       const uint32_t q = smem_u32(sm_q);
       bool ok = mbar_wait(q_ready, 0, err);
       tc_fence_after();
@@ -514,14 +566,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {      // Q's hi, then its lo
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // the left operand K-major, the right one MN-major, both as stored
-            const uint32_t left = p.tall ? x : q + part * kSliceBytes, right = p.tall ? q + part * kSliceBytes : x;
-            umma_f16(tmem + (i & 1) * kSide, sdesc_sw128(left + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
-                     sdesc_sw128(right + k * 2048, kChunkBytes, 1024), idesc, (part | k) != 0);
-          }
+          const uint32_t qp = q + part * kSliceBytes, left = p.tall ? x : qp, right = p.tall ? qp : x;
+          if (p.used == 64)
+            products<kHalf>(tmem + (i & 1) * kSide, k_major(left), mn_major(right), idesc, part);
+          else
+            products<kFull>(tmem + (i & 1) * kSide, k_major(left), mn_major(right), idesc, part);
         }
         umma_commit(&tfull[2 + (i & 1)]);
       }
@@ -533,34 +584,33 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     }
     __syncwarp();
   } else {
-    // each warp writes its 32 rows x 64 columns over the slice it came from
-    // (whose products are done) and stores that box itself
+    // two warps write their 32 rows x 64 columns over the slice that they came
+    // from (whose products are done), and the first stores that box.  A wait
+    // that gives up records that and goes on: the pair's barrier needs both.
+    const uint64_t policy = policy_drop();
+    const int pair = 2 + quarter + 4 * (col0 >> 6);   // named barrier of the two
+    const bool store = (col0 & 32) == 0 && lane == 0;
     for (int i = 0; i < count; ++i) {
-      if (!mbar_wait(&tfull[2 + (i & 1)], (i >> 1) & 1, err)) break;
+      mbar_wait(&tfull[2 + (i & 1)], (i >> 1) & 1, err);
       tc_fence_after();
       uint8_t* box = smem + (i % kRing) * kSliceBytes + ch;
+      float v[32];
+      tmem_ld32(tmem + lanes + (i & 1) * kSide + col0, v);
+      tc_fence_before();
+      mbar_arrive(&tempty[2 + (i & 1)]);
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        float v[32];
-        tmem_ld32(tmem + lanes + (i & 1) * kSide + col0 + 32 * g, v);
-        if (g == 1) {
-          tc_fence_before();
-          mbar_arrive(&tempty[2 + (i & 1)]);
-        }
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t u[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = pack_16<BF16>(v[8 * q + 2 * j] * scale, v[8 * q + 2 * j + 1] * scale);
-          *reinterpret_cast<uint4*>(box + row_piece(row, 4 * g + q)) = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+        for (int j = 0; j < 4; ++j) u[j] = pack_16<BF16>(v[8 * q + 2 * j] * scale, v[8 * q + 2 * j + 1] * scale);
+        *reinterpret_cast<uint4*>(box + row_piece(row, piece0 + q)) = make_uint4(u[0], u[1], u[2], u[3]);
       }
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      if (store) {
         const int at = (first + i) * kSide;
         const int x0 = p.tall ? col0 : at + col0, y0 = p.tall ? at + quarter * 32 : quarter * 32;
-        if (x0 < p.cols && y0 < p.rows) tma_store_3d(&omap, box + quarter * 4096, x0, y0, matrix);
+        if (x0 < p.cols && y0 < p.rows) store_box(&omap, box + quarter * 4096, x0, y0, matrix, policy);
         bulk_commit();
         if (i > 0) {                                // the previous slice's box has been read
           bulk_wait_read<1>();
@@ -568,7 +618,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (store) bulk_wait_all();
     __syncwarp();
   }
 
@@ -722,6 +772,7 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   p.tall = d->rows > d->cols;
   p.rows = static_cast<int32_t>(d->rows);
   p.cols = static_cast<int32_t>(d->cols);
+  p.used = std::min(d->rows, d->cols) <= 64 ? 64 : kSide;
   p.slices = static_cast<int32_t>((std::max(d->rows, d->cols) + kSide - 1) / kSide);
   p.steps = d->ns_steps;
   p.a = d->ns_a;
@@ -739,6 +790,7 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
                        : cudaFuncSetAttribute(orthogonalize_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               kOrthSmem);
   const int ranks = pick_cluster(bf16, d->batch, p.slices, dev);
+  p.late_below = d->batch >= static_cast<int64_t>(kLateWaves) * sms ? sms : 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(d->batch * ranks));
   cfg.blockDim = dim3(kOrthThreads);
