@@ -25,7 +25,7 @@
 // the number of products added up (5e-7 of the result's norm at k = 8192, for
 // random operands).  fp32 results are therefore accumulated over at most
 // kChunkBlocks k-blocks in TMEM, and the chunks are added in IEEE fp32 in the
-// result itself, by the thread that wrote it: 8e-8.
+// result itself, by the thread that wrote it: 2e-7.
 #include <algorithm>
 
 #include "muonh_common.cuh"
@@ -38,7 +38,7 @@ constexpr int kKBlock = 128;                     // k per stage: one scale block
 constexpr int kThreads = 384;
 constexpr int kEpi = 256;                        // epilogue threads
 constexpr int kScaleRing = 4;                    // scale words in flight: 512 of k each
-constexpr int kChunkBlocks = 16;                 // fp32 results: k-blocks per TMEM accumulation
+constexpr int kChunkBlocks = 32;                 // fp32 results: k-blocks per TMEM accumulation
 
 // PAIR: BN is 256, shared by the two CTAs.
 template <int BN, bool PAIR>
@@ -139,12 +139,12 @@ __device__ __forceinline__ void tile_at(const BlockParams& p, int64_t t, int& tm
   tn = r / rows;
 }
 
-// Scale bytes of k-blocks 4 g .. 4 g + 3 of one operand row, as one word; 2^0
-// where there is no row or no such block (what they scale is zero).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int shift, int words, int row, int rows,
-                                               int g, int k_blocks) {
-  if (row >= rows) return 0x7f7f7f7fu;
-  const uint8_t* p = s + static_cast<int64_t>(row >> shift) * ld + 4 * g;
+// Scale bytes of k-blocks 4 g .. 4 g + 3 of one operand row (null: behind the
+// last one), as one word; 2^0 where there is no row or no such block (what they
+// scale is zero).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int words, int g, int k_blocks) {
+  if (!row) return 0x7f7f7f7fu;
+  const uint8_t* p = row + 4 * g;
   if (words && 4 * g + 4 <= k_blocks) return __ldg(reinterpret_cast<const uint32_t*>(p));
   uint32_t w = 0u;
 #pragma unroll
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + C::kAccs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;   // 0 = leader: issues the MMAs, holds full, sfull and tempty
   const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
 
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) {
-      mbar_init(&sfull[s], 32 * kCtas);
+      mbar_init(&sfull[s], kCtas);
       mbar_init(&sempty[s], 1);
     }
     for (int a = 0; a < C::kAccs; ++a) {
@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------------------ MMA issuer
+      const bool leader = elect_lane();
       int stage = 0, ring = 0, acc = 0;
       uint32_t phase = 0, ring_phase = 0, acc_phase = 0;
       bool ok = true;
@@ -352,14 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const uint32_t from = smem_u32(smem + C::kScaleOffset + ring * C::kScaleBytes);
+            if (leader) {
 #pragma unroll
-            for (int b = 0; b < C::kScaleBlocks; ++b) {
-              if (PAIR)
-                copy_scales_pair(sc + 4 * b, scale_desc(from + 512 * b));
-              else
-                copy_scales(sc + 4 * b, scale_desc(from + 512 * b));
+              for (int b = 0; b < C::kScaleBlocks; ++b) {
+                if (PAIR)
+                  copy_scales_pair(sc + 4 * b, scale_desc(from + 512 * b));
+                else
+                  copy_scales(sc + 4 * b, scale_desc(from + 512 * b));
+              }
+              commit(&sempty[ring]);
             }
-            commit(&sempty[ring]);
+            __syncwarp();
           }
           if (!mbar_wait(&full[stage], phase, err)) {
             ok = false;
@@ -368,15 +372,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t a = smem_u32(smem + stage * C::kStageBytes), b = a + C::kABytes;
           const uint32_t idesc = idesc_mxf8(C::kTileRows, BN, kb & 3);
+          const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < kKBlock / 32; ++k) {
-            const uint64_t ad = sdesc_sw128(a + k * 32, 16, 1024), bd = sdesc_sw128(b + k * 32, 16, 1024);
-            if (PAIR)
-              umma_mxf8_pair(tmem + acc * 128, ad, bd, idesc, sc, sc + 4, !fresh || k != 0);
-            else
-              umma_mxf8(tmem + acc * 128, ad, bd, idesc, sc, sc + 4, !fresh || k != 0);
+            for (int k = 0; k < kKBlock / 32; ++k) {   // 32 bytes of a row each
+              if (PAIR)
+                umma_mxf8_pair(tmem + acc * 128, ad + 2 * k, bd + 2 * k, idesc, sc, sc + 4, !fresh || k != 0);
+              else
+                umma_mxf8(tmem + acc * 128, ad + 2 * k, bd + 2 * k, idesc, sc, sc + 4, !fresh || k != 0);
+            }
+            commit(&empty[stage]);
+            if (left == 1) commit(&tfull[acc]);
           }
-          commit(&empty[stage]);
+          __syncwarp();
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -385,17 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             ring = 0;
             ring_phase ^= 1u;
           }
-          if (--left == 0) {
-            commit(&tfull[acc]);
-            if (++acc == C::kAccs) {
-              acc = 0;
-              acc_phase ^= 1u;
-            }
+          if (--left == 0 && ++acc == C::kAccs) {
+            acc = 0;
+            acc_phase ^= 1u;
           }
         }
       }
       // no MMA may still write TMEM when the CTA frees it
-      umma_commit(drain);
+      if (leader) umma_commit(drain);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
       }
@@ -412,33 +417,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tm, tn;
       tile_at(p, t, tm, tn);
       const int arow = tm * C::kTileRows + static_cast<int>(rank) * kTm;
-      for (int w = 0; 4 * w < p.k_blocks; ++w) {
-        uint32_t u[C::kScaleBlocks][4];
+      const uint8_t* rows[C::kScaleBlocks][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          u[0][j] = scale_word(p.sa, p.ld_sa, p.sa_shift, p.sa_words, arow + 32 * j + lane, p.m, w, p.k_blocks);
+      for (int b = 0; b < C::kScaleBlocks; ++b)
 #pragma unroll
-        for (int b = 1; b < C::kScaleBlocks; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            u[b][j] = 128 * (b - 1) + 32 * j < BN
-                          ? scale_word(p.sb, p.ld_sb, p.sb_shift, p.sb_words, tn * BN + 128 * (b - 1) + 32 * j + lane,
-                                       p.n, w, p.k_blocks)
-                          : 0x7f7f7f7fu;
-        if (!mbar_wait(&sempty[ring], ring_phase ^ 1u, err)) ok = false;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+        for (int j = 0; j < 4; ++j) {
+          const int in_b = 128 * (b - 1) + 32 * j;     // of B's rows
+          const int row = b == 0 ? arow + 32 * j + lane : tn * BN + in_b + lane;
+          rows[b][j] = b == 0 ? (row < p.m ? p.sa + static_cast<int64_t>(row >> p.sa_shift) * p.ld_sa : nullptr)
+                              : (in_b < BN && row < p.n ? p.sb + static_cast<int64_t>(row >> p.sb_shift) * p.ld_sb : nullptr);
         }
-        uint8_t* to = smem + C::kScaleOffset + ring * C::kScaleBytes + lane * 16;
+      for (int w0 = 0; 4 * w0 < p.k_blocks && ok; w0 += kScaleRing) {
+        // kScaleRing groups at once: their loads are in flight together (one
+        // group at a time, the MMAs waited for scales a third of the time)
+        uint32_t u[kScaleRing][C::kScaleBlocks][4];
 #pragma unroll
-        for (int b = 0; b < C::kScaleBlocks; ++b)
-          *reinterpret_cast<uint4*>(to + 512 * b) = make_uint4(u[b][0], u[b][1], u[b][2], u[b][3]);
-        fence_proxy_async_smem();
-        arrive_leader(&sfull[ring]);
-        if (++ring == kScaleRing) {
-          ring = 0;
-          ring_phase ^= 1u;
+        for (int g = 0; g < kScaleRing; ++g)
+#pragma unroll
+          for (int b = 0; b < C::kScaleBlocks; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              u[g][b][j] = 4 * (w0 + g) < p.k_blocks
+                               ? scale_word(rows[b][j], b == 0 ? p.sa_words : p.sb_words, w0 + g, p.k_blocks)
+                               : 0u;
+#pragma unroll
+        for (int g = 0; g < kScaleRing; ++g) {
+          if (4 * (w0 + g) >= p.k_blocks) break;
+          if (!mbar_wait(&sempty[ring], ring_phase ^ 1u, err)) ok = false;
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          uint8_t* to = smem + C::kScaleOffset + ring * C::kScaleBytes + lane * 16;
+#pragma unroll
+          for (int b = 0; b < C::kScaleBlocks; ++b)
+            *reinterpret_cast<uint4*>(to + 512 * b) = make_uint4(u[g][b][0], u[g][b][1], u[g][b][2], u[g][b][3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_leader(&sfull[ring]);
+          if (++ring == kScaleRing) {
+            ring = 0;
+            ring_phase ^= 1u;
+          }
         }
       }
     }

@@ -4,7 +4,7 @@ Quantising is exact: values and scales have to be equal.  A product's tolerance
 is in units of S = sum_k |a b| of each element.  An MMA adds 32 products to the
 accumulator and truncates: it loses at most one step of fp32 (2^-23) of the sum
 and, where it aligns the products to the largest, as much again, so 2^-22 S per
-MMA.  There are four per 128 of k, counted over at most 16 such blocks for fp32
+MMA.  There are four per 128 of k, counted over at most 32 such blocks for fp32
 results, whose chunks are added in fp32 (2^-24 S each); a 16-bit result counts
 all of k, and is rounded once (half a step)."""
 import numpy as np
@@ -160,7 +160,7 @@ def check_product(a, b, d, k):
     ref, size = a @ b.T, np.abs(a) @ np.abs(b).T
     blocks = -(-k // 128)
     if d.dtype == t.float32:
-        tol = (4 * min(blocks, 16) * 2.0 ** -22 + -(-blocks // 16) * 2.0 ** -24) * size
+        tol = (4 * min(blocks, 32) * 2.0 ** -22 + -(-blocks // 32) * 2.0 ** -24) * size
     else:
         tol = 4 * blocks * 2.0 ** -22 * size
         f = t.finfo(d.dtype)
