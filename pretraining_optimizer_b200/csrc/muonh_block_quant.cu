@@ -59,6 +59,19 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
+// The first `left` elements of 16 bytes, one by one, and zeros.  (Rare where speed
+// counts: a function of its own, by value, keeps it out of the fast path.)
+template <typename T>
+__device__ __noinline__ uint4 load_tail(const T* p, int64_t left) {
+  using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+  const Bits* b = reinterpret_cast<const Bits*>(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < static_cast<int>(16 / sizeof(T)); ++j)
+    if (j < left) w[j * sizeof(T) / 4] |= static_cast<uint32_t>(b[j]) << (sizeof(T) == 2 ? 16 * (j & 1) : 0);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // An 8-element piece of a row as it was loaded.
 template <typename T>
 struct Piece {
@@ -74,17 +87,11 @@ struct Piece {
       }
       return;
     }
-    zero();
-    using Bits = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
-    const Bits* b = reinterpret_cast<const Bits*>(p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < left) {
-        if constexpr (sizeof(T) == 2)
-          w[j >> 1] |= static_cast<uint32_t>(b[j]) << (16 * (j & 1));
-        else
-          w[j] = b[j];
-      }
+    for (int k = 0; k < kWords / 4; ++k) {
+      const uint4 u = load_tail<T>(p + k * (16 / sizeof(T)), left - static_cast<int64_t>(k * (16 / sizeof(T))));
+      w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+    }
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -118,14 +125,18 @@ __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m) {
   return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
 }
 
-// 8 bytes of one output row; bytes behind the row's end are left as they were.
+// The first `left` (below 8) bytes of one output piece; what is behind the row's
+// end is left as it was.  A function of its own: it is rare, and its code would
+// crowd the others out of the instruction cache.
+__device__ __noinline__ void store_tail(uint8_t* p, uint2 v, int left) {
+  const uint64_t u = (static_cast<uint64_t>(v.y) << 32) | v.x;
+  for (int i = 0; i < left; ++i) p[i] = static_cast<uint8_t>(u >> (8 * i));
+}
 __device__ __forceinline__ void store8(uint8_t* p, uint2 v, int64_t left) {
-  if (left >= 8) {
+  if (left >= 8)
     *reinterpret_cast<uint2*>(p) = v;
-  } else {
-    const uint64_t u = (static_cast<uint64_t>(v.y) << 32) | v.x;
-    for (int i = 0; i < left; ++i) p[i] = static_cast<uint8_t>(u >> (8 * i));
-  }
+  else if (left > 0)
+    store_tail(p, v, static_cast<int>(left));
 }
 
 template <typename T>
@@ -165,7 +176,7 @@ __global__ void __launch_bounds__(kQuantThreads) block_quantize_rows_kernel(cons
     const int b = scale_byte(as_f32_bits<T>(m));
     if (row[i] >= p.rows) continue;
     if (lane == 0) p.s[row[i] * p.lds + col[i] / kTile] = static_cast<uint8_t>(b);
-    if (col[i] < p.cols) store8(p.q + row[i] * p.ldq + col[i], quantize_row(v[i], inverse_scale(b)), p.cols - col[i]);
+    store8(p.q + row[i] * p.ldq + col[i], quantize_row(v[i], inverse_scale(b)), p.cols - col[i]);
   }
 }
 
@@ -173,24 +184,48 @@ __device__ __forceinline__ uint32_t turned_piece(int row, int piece) {
   return static_cast<uint32_t>(row * kTile + ((piece ^ ((row >> 3) & 15)) << 3));
 }
 
+// Maxima along the rows of eight values per lane over 16 lanes: lane l ends
+// with that of row (l >> 1) & 7 (8 shuffles, each halving what is left, in place of 32).
+__device__ __forceinline__ uint32_t row_maxima(const uint32_t (&m)[8]) {
+  const int lane = threadIdx.x & 15;
+  uint32_t a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t keep = (lane & 8) ? m[i + 4] : m[i], give = (lane & 8) ? m[i] : m[i + 4];
+    a[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t keep = (lane & 4) ? a[i + 2] : a[i], give = (lane & 4) ? a[i] : a[i + 2];
+    b[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+  }
+  const uint32_t keep = (lane & 2) ? b[1] : b[0], give = (lane & 2) ? b[0] : b[1];
+  const uint32_t c = max(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+  return max(c, __shfl_xor_sync(0xffffffffu, c, 1));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
     block_quantize_kernel(const __grid_constant__ QuantParams p) {
   constexpr int kWords = Piece<T>::kWords;
-  __shared__ uint32_t column_max[kQuantThreads / 32][kTile / 8 * kWords];
+  constexpr int kColumnWords = kTile / 8 * kWords;   // a row of the tile
+  __shared__ uint32_t column_max[kQuantThreads / 32][kColumnWords];
+  __shared__ __align__(16) float column_factor[kTile];
   __shared__ __align__(16) uint8_t turned[kTile * kTile];
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile, c0 = static_cast<int64_t>(blockIdx.x) * kTile;
   const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;   // this thread's 8 columns and 8 rows
-  const int64_t col = c0 + tc * 8;
+  const int64_t col = c0 + tc * 8, row0 = r0 + tr * 8;
 
   Piece<T> v[8];
+  {
+    const T* x = static_cast<const T*>(p.x) + row0 * p.ldx + col;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = r0 + tr * 8 + i;
-    if (row < p.rows)
-      v[i].load(static_cast<const T*>(p.x) + row * p.ldx + col, p.vec && col < p.cols, p.cols - col);
-    else
-      v[i].zero();
+    for (int i = 0; i < 8; ++i, x += p.ldx) {
+      if (row0 + i < p.rows)
+        v[i].load(x, p.vec && col < p.cols, p.cols - col);
+      else
+        v[i].zero();
+    }
   }
 
   uint32_t m_row[8], m_col[kWords];
@@ -208,7 +243,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
     if (sizeof(T) == 2) m_row[i] = max(m_row[i] & 0xffffu, m_row[i] >> 16);
   }
 
-  int b_row[8], b_col[8];
+  float f_row[8], f_col[8];
   if (p.whole) {
     uint32_t m = 0u;
 #pragma unroll
@@ -219,72 +254,75 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, column_max[w][0]);
     const int b = scale_byte(as_f32_bits<T>(m));
+    const float f = inverse_scale(b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b_row[i] = b_col[i] = b;
+    for (int i = 0; i < 8; ++i) f_row[i] = f_col[i] = f;
     if (threadIdx.x == 0) {
       if (p.q) p.s[blockIdx.y * p.lds + blockIdx.x] = static_cast<uint8_t>(b);
       if (p.qt) p.st[blockIdx.x * p.ldst + blockIdx.y] = static_cast<uint8_t>(b);
     }
   } else {
-    if (p.q) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m_row[i] = max(m_row[i], __shfl_xor_sync(0xffffffffu, m_row[i], o));
-        b_row[i] = scale_byte(as_f32_bits<T>(m_row[i]));
-        const int64_t row = r0 + tr * 8 + i;
-        if (tc == 0 && row < p.rows) p.s[row * p.lds + blockIdx.x] = static_cast<uint8_t>(b_row[i]);
-      }
-    }
     if (p.qt) {
 #pragma unroll
       for (int k = 0; k < kWords; ++k) {
         const uint32_t m = larger<T>(m_col[k], __shfl_xor_sync(0xffffffffu, m_col[k], 16));
         if ((threadIdx.x & 16) == 0) column_max[threadIdx.x >> 5][tc * kWords + k] = m;
       }
-      __syncthreads();
+    }
+    if (p.q) {
+      const int mine = (tc >> 1) & 7;
+      const int b = scale_byte(as_f32_bits<T>(row_maxima(m_row)));
+      if ((tc & 1) == 0 && row0 + mine < p.rows) p.s[(row0 + mine) * p.lds + blockIdx.x] = static_cast<uint8_t>(b);
+      const float f = inverse_scale(b);
+      // row i's factor is in lane 2 i: bit 2 of i was split by xor 8, bit 1 by xor 4, bit 0 by xor 2
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) {
+      for (int i = 0; i < 8; ++i) f_row[i] = __shfl_sync(0xffffffffu, f, (threadIdx.x & 16) + 2 * i);
+    }
+    if (p.qt) {
+      // one thread per column (16-bit: its half of a word)
+      __syncthreads();
+      if (threadIdx.x < kTile) {
+        const int j = threadIdx.x;
         uint32_t m = 0u;
 #pragma unroll
-        for (int w = 0; w < kQuantThreads / 32; ++w) m = larger<T>(m, column_max[w][tc * kWords + k]);
-        if constexpr (sizeof(T) == 4) {
-          b_col[k] = scale_byte(m);
-        } else {
-          b_col[2 * k] = scale_byte(as_f32_bits<T>(m & 0xffffu));
-          b_col[2 * k + 1] = scale_byte(as_f32_bits<T>(m >> 16));
-        }
+        for (int w = 0; w < kQuantThreads / 32; ++w)
+          m = larger<T>(m, column_max[w][sizeof(T) == 4 ? j : j >> 1]);
+        if (sizeof(T) == 2) m = (j & 1) ? m >> 16 : m & 0xffffu;
+        const int b = scale_byte(as_f32_bits<T>(m));
+        column_factor[j] = inverse_scale(b);
+        if (c0 + j < p.cols) p.st[(c0 + j) * p.ldst + blockIdx.y] = static_cast<uint8_t>(b);
       }
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (tr == 0 && col + j < p.cols) p.st[(col + j) * p.ldst + blockIdx.y] = static_cast<uint8_t>(b_col[j]);
+      for (int j = 0; j < 8; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(column_factor + tc * 8 + j);
+        f_col[j] = f.x, f_col[j + 1] = f.y, f_col[j + 2] = f.z, f_col[j + 3] = f.w;
+      }
     }
   }
 
   if (p.q) {
+    uint8_t* q = p.q + row0 * p.ldq + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = r0 + tr * 8 + i;
-      const uint2 u = quantize_row(v[i], inverse_scale(b_row[i]));
-      if (row < p.rows && col < p.cols) store8(p.q + row * p.ldq + col, u, p.cols - col);
-    }
+    for (int i = 0; i < 8; ++i, q += p.ldq)
+      if (row0 + i < p.rows) store8(q, quantize_row(v[i], f_row[i]), p.cols - col);
   }
   if (p.qt) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float f = inverse_scale(b_col[j]);
+      const float f = f_col[j];
       const uint2 u = make_uint2(to_e4m3x4(v[0].at(j) * f, v[1].at(j) * f, v[2].at(j) * f, v[3].at(j) * f),
                                  to_e4m3x4(v[4].at(j) * f, v[5].at(j) * f, v[6].at(j) * f, v[7].at(j) * f));
       *reinterpret_cast<uint2*>(turned + turned_piece(tc * 8 + j, tr)) = u;
     }
     __syncthreads();
     // 128 rows of the transposed tile, 16 pieces of 8 bytes each
+    uint8_t* qt = p.qt + (c0 + tr) * p.ldqt + r0 + tc * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, qt += 16 * p.ldqt) {
       const int row = i * 16 + tr;
-      const int64_t to = c0 + row, at = r0 + tc * 8;
-      if (to < p.cols && at < p.rows)
-        store8(p.qt + to * p.ldqt + at, *reinterpret_cast<const uint2*>(turned + turned_piece(row, tc)), p.rows - at);
+      if (c0 + row < p.cols)
+        store8(qt, *reinterpret_cast<const uint2*>(turned + turned_piece(row, tc)), p.rows - r0 - tc * 8);
     }
   }
 }
