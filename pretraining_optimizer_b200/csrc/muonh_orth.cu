@@ -159,10 +159,10 @@ __device__ constexpr uint32_t k_major_step(int k) { return ((k >> 2) * kChunkByt
 __device__ constexpr uint32_t mn_major_step(int k) { return (k * 16 * 128) >> 4; }
 
 // D (+)= L R over K steps: L K-major, R MN-major, both as their rows are
-// stored.  Inlined straight-line code, so that the descriptors are computed in
-// uniform registers: in a function of its own, in a loop, or with a branch around
-// each MMA, one took 135 cycles to issue, against the 64 to 81 that it takes to
-// run.  The small side is rounded up to 64 or 128 for that (kHalf, kFull).
+// stored.  Inlined straight-line code, so that the descriptors stay in uniform
+// registers: in a function of its own, in a loop, or with a branch around each
+// MMA, one took 135 cycles to issue, against the 64 that it takes to run.  The
+// small side is rounded up to 64 or 128 for that (kHalf, kFull).
 constexpr int kHalf = 4, kFull = 8;
 template <int K>
 __device__ __forceinline__ void products(uint32_t d, uint64_t left, uint64_t right, uint32_t idesc, uint32_t accumulate) {
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
   float* trace = reinterpret_cast<float*>(err + 1);   // [4]: shares of the diagonal
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   uint32_t ranks;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const uint32_t rank = cluster_ctarank();
@@ -355,17 +355,18 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (lane == 0) produce(0);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16(kSide, p.used, BF16, p.tall) | (static_cast<uint32_t>(p.tall) << 15);
-      bool ok = true;
-      for (int i = 0; i < count && ok; ++i) {
-        const int slot = i % kRing, chunk = i / kGramChunk;
-        if (i % kGramChunk == 0 && chunk >= 2) ok = mbar_wait(&tempty[chunk & 1], ((chunk >> 1) - 1) & 1, err);
-        ok = ok && mbar_wait(&full[slot], (i / kRing) & 1, err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t x = smem_u32(smem + slot * kSliceBytes);
-        const uint64_t d = p.tall ? mn_major(x) : k_major(x);
+    const uint32_t idesc = idesc_f16(kSide, p.used, BF16, p.tall) | (static_cast<uint32_t>(p.tall) << 15);
+    const bool leader = elect_lane();
+    bool ok = true;
+    for (int i = 0; i < count && ok; ++i) {
+      const int slot = i % kRing, chunk = i / kGramChunk;
+      if (i % kGramChunk == 0 && chunk >= 2) ok = mbar_wait(&tempty[chunk & 1], ((chunk >> 1) - 1) & 1, err);
+      ok = ok && mbar_wait(&full[slot], (i / kRing) & 1, err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+      const uint64_t d = p.tall ? mn_major(x) : k_major(x);
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint64_t dk = d + (p.tall ? mn_major_step(k) : k_major_step(k));
@@ -374,8 +375,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         umma_commit(&empty[slot]);
         if (i % kGramChunk == kGramChunk - 1 || i == count - 1) umma_commit(&tfull[chunk & 1]);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = 0.f;
@@ -412,32 +413,33 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   // ------------------------------------------------- the r x r iteration
   float scale = 0.f;                                // 1 / (||X|| + eps)
   if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16(kSide, p.used, 0, 1);
-      const uint32_t a = smem_u32(sm_a), q = smem_u32(sm_q);
-      // per step: A_k^2 once A_k is there, A_k P_k once P_k is, (A_k P_k) P_k once A_k P_k is, and then
-      // Q_k P_k, which runs while the epilogue works on A_{k+1}.  The last step has the first and the Q
-      // product only, the first step no Q product (P_0 is Q_1).
-      int waits = 0;
-      bool ok = true;
-      for (int n = 0; n < 4 * p.steps && ok; ++n) {
-        const int k = n >> 2, phase = n & 3;
-        const bool last = k == p.steps - 1;
-        if (phase < 2 || (phase == 2 && !last)) {    // the last P_k has to be there for its Q product, too
-          ok = mbar_wait(ready, waits++ & 1, err);
-          tc_fence_after();
-        }
-        if (!ok || (last && (phase == 1 || phase == 2)) || (k == 0 && phase == 3)) continue;
-        const uint32_t pk = k == 0 ? q : smem_u32(sm_p);
-        const uint32_t d = phase == 3 ? tm_q : tm_d, l = phase == 3 ? q : a, r = phase == 0 ? a : pk;
+    const uint32_t idesc = idesc_f16(kSide, p.used, 0, 1);
+    const uint32_t a = smem_u32(sm_a), q = smem_u32(sm_q);
+    const bool leader = elect_lane();
+    // per step: A_k^2 once A_k is there, A_k P_k once P_k is, (A_k P_k) P_k once A_k P_k is, and then
+    // Q_k P_k, which runs while the epilogue works on A_{k+1}.  The last step has the first and the Q
+    // product only, the first step no Q product (P_0 is Q_1).
+    int waits = 0;
+    bool ok = true;
+    for (int n = 0; n < 4 * p.steps && ok; ++n) {
+      const int k = n >> 2, phase = n & 3;
+      const bool last = k == p.steps - 1;
+      if (phase < 2 || (phase == 2 && !last)) {      // the last P_k has to be there for its Q product, too
+        ok = mbar_wait(ready, waits++ & 1, err);
+        tc_fence_after();
+      }
+      if (!ok || (last && (phase == 1 || phase == 2)) || (k == 0 && phase == 3)) continue;
+      const uint32_t pk = k == 0 ? q : smem_u32(sm_p);
+      const uint32_t d = phase == 3 ? tm_q : tm_d, l = phase == 3 ? q : a, r = phase == 0 ? a : pk;
+      if (leader) {
         if (p.used == 64)
           pair_product<kHalf>(d, l, r, idesc);
         else
           pair_product<kFull>(d, l, r, idesc);
         umma_commit(phase == 3 ? done_q : done);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp >= 2) {
     // ||X||^2 is the trace; summed over a warp's rows, then over the warps
     const bool diagonal = col0 == quarter * 32;     // this warp's block holds diagonal elements, one per lane
@@ -553,19 +555,20 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     if (lane == 0 && mbar_wait(q_ready, 0, err)) produce(1);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // wide: N is the slice's width and k the small side; tall: N and k are the small side
-      const uint32_t idesc = idesc_f16(kSide, p.tall ? p.used : kSide, BF16, 1);
-      const uint32_t q = smem_u32(sm_q);
-      bool ok = mbar_wait(q_ready, 0, err);
+    // wide: N is the slice's width and k the small side; tall: N and k are the small side
+    const uint32_t idesc = idesc_f16(kSide, p.tall ? p.used : kSide, BF16, 1);
+    const uint32_t q = smem_u32(sm_q);
+    const bool leader = elect_lane();
+    bool ok = mbar_wait(q_ready, 0, err);
+    tc_fence_after();
+    for (int i = 0; i < count && ok; ++i) {
+      const int slot = i % kRing;
+      ok = (i < 2 || mbar_wait(&tempty[2 + (i & 1)], ((i >> 1) - 1) & 1, err)) &&
+           mbar_wait(&full[kRing + slot], (i / kRing) & 1, err);
+      if (!ok) break;
       tc_fence_after();
-      for (int i = 0; i < count && ok; ++i) {
-        const int slot = i % kRing;
-        ok = (i < 2 || mbar_wait(&tempty[2 + (i & 1)], ((i >> 1) - 1) & 1, err)) &&
-             mbar_wait(&full[kRing + slot], (i / kRing) & 1, err);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+      const uint32_t x = smem_u32(smem + slot * kSliceBytes);
+      if (leader) {
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {      // Q's hi, then its lo
           const uint32_t qp = q + part * kSliceBytes, left = p.tall ? x : qp, right = p.tall ? qp : x;
@@ -576,11 +579,12 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         }
         umma_commit(&tfull[2 + (i & 1)]);
       }
-      // no MMA may still write TMEM when the CTA frees it
-      umma_commit(drain);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
-      }
+      __syncwarp();
+    }
+    // no MMA may still write TMEM when the CTA frees it
+    if (leader) umma_commit(drain);
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
     }
     __syncwarp();
   } else {
