@@ -60,8 +60,8 @@ constexpr int kGramChunk = 16;                    // slices (2048 columns) per T
 constexpr int kMaxSteps = 16;
 // With several matrices per SM all SMs read X, iterate and write at the same
 // time, and HBM idles during the r x r iterations.  Half of the SMs start a
-// quarter of a matrix later: 896 x [128, 2048] took 470 us without, 436 with 15
-// us, 441 with 35 us; below four matrices per SM the delay costs what it gives.
+// quarter of a matrix later: 896 x [128, 2048] took 437 us without, 403 with 15
+// us, 406 with 25 us; below four matrices per SM the delay costs what it gives.
 constexpr int kLateNs = 15000;
 constexpr int kLateWaves = 4;
 constexpr int kMaxCluster = 8;

@@ -15,20 +15,20 @@ import ctypes
 
 from .muonh import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, QUINTIC, BlockOperand, OrthogonalizeDesc, _check, library)
 
-_TYPES = None
+torch = None    # imported by the first call: building the library imports this package without it
+_TYPES = {}     # {torch dtype: MUONH_DTYPE_*}
 
 
 def _types():
-    """{torch dtype: MUONH_DTYPE_*}; torch is imported with the first call, like elsewhere in the binding."""
-    global _TYPES
-    if _TYPES is None:
-        import torch
-        _TYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    global torch
+    if torch is None:
+        import torch as module
+        _TYPES.update({module.float32: DTYPE_F32, module.bfloat16: DTYPE_BF16, module.float16: DTYPE_F16})
+        torch = module
     return _TYPES
 
 
 def _tensor(t, what: str, dtypes, device=None):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
         raise TypeError(f"{what} must be a CUDA tensor of dtype {', '.join(map(str, dtypes))}")
     if device is not None and t.device != device:
@@ -37,7 +37,6 @@ def _tensor(t, what: str, dtypes, device=None):
 
 def _here(t, stream):
     """The handle of the current stream where the call belongs there; None where it has to move first."""
-    import torch
     index = t.get_device()
     if stream is None and torch._C._cuda_getDevice() == index:
         return torch._C._cuda_getCurrentRawStream(index)
@@ -46,7 +45,6 @@ def _here(t, stream):
 
 def _elsewhere(device, stream, call, *args, **kw):
     """`call` with `device` and `stream` as the current ones."""
-    import torch
     if stream is not None and stream.device != device:
         raise ValueError(f"stream must belong to {device}, like the tensors")
     with torch.cuda.device(device), torch.cuda.stream(stream):
@@ -78,8 +76,12 @@ def _rows(t, what: str):
     return t.data_ptr(), rows, n, ld
 
 
+def _like(x):
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _vector(t, what: str, n: int, device):
-    import torch
     if t is None:
         return None
     _tensor(t, what, (torch.float32,), device)
@@ -94,7 +96,6 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     fp32, as adamw_step keeps them.  Returns (y, mean, rstd): y in x's type (or
     `out`, which may be x), mean (None for the RMS norm) and rstd fp32, one per
     row, for layer_norm_backward."""
-    import torch
     _tensor(x, "x", _types())
     handle = _here(x, stream)
     if handle is None:
@@ -106,7 +107,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     wp = _vector(weight, "weight", n, device)
     bp = _vector(bias, "bias", n, device)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _like(x)
         op, ldo = out.data_ptr(), n
     else:
         _tensor(out, "out", (dtype,), device)
@@ -126,7 +127,6 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
     and type): (dx, dweight, dbias).  mean and rstd are what layer_norm gave;
     mean None means the RMS norm.  dweight (None where weight is None) and dbias
     (None unless bias is true) are fp32, as adamw_step reads them."""
-    import torch
     _tensor(x, "x", _types())
     handle = _here(x, stream)
     if handle is None:
@@ -143,7 +143,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
     if rp is None:
         raise TypeError("rstd must be given")
     lib = library()
-    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dx = _like(x)
     dweight = None if weight is None else torch.empty_like(weight)
     dbias = torch.empty(n, dtype=torch.float32, device=device) if bias else None
     size = lib.muonh_layer_norm_workspace(rows, n) if weight is not None or bias else 0
@@ -172,7 +172,7 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     for matrices whose smaller side is at most 128: one Muon update per
     attention head.  Returns a tensor of x's shape and type, laid out like x
     where x has no gaps, or `out`, which may be x."""
-    import torch
+    _types()
     _tensor(x, "x", (torch.bfloat16, torch.float16))
     handle = _here(x, stream)
     if handle is None:
@@ -216,7 +216,6 @@ def _matrix(t, what: str):
 
 
 def _quantize(x, block_rows, rows, columns, stream):
-    import torch
     _tensor(x, "x", _types())
     handle = _here(x, stream)
     if handle is None:
@@ -258,7 +257,7 @@ def block_quantize_weight(w, stream=None):
 
 
 def _block_operand(q, scale, what: str, device=None):
-    import torch
+    _types()
     _tensor(q, what, (torch.float8_e4m3fn,), device)
     _tensor(scale, f"{what}_scale", (torch.uint8,), q.device)
     qp, rows, k, ld = _matrix(q, what)
@@ -274,7 +273,6 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
     rows, and each 128 columns.  Returns [m, n] in dtype (bf16 by default; fp32
     or fp16) or writes to `out`; accumulate=True adds to an fp32 `out`, such as
     the gradient that MuonH.step reads."""
-    import torch
     ao, m, k = _block_operand(a, a_scale, "a")
     handle = _here(a, stream)
     if handle is None:
@@ -304,7 +302,7 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
 def operator_status(stream=None) -> None:
     """Synchronises `stream` (default: the current one) and raises MuonHError
     if a device wait gave up in an operator call since the previous check."""
-    import torch
     if stream is None:
+        _types()
         stream = torch.cuda.current_stream()
     _check(library().muonh_operator_status(stream.cuda_stream))
