@@ -15,6 +15,9 @@
 //           then fetches 32 KB per 128 of k for 128 x 256 results, against 48 KB
 //           for a 128 x 256 tile of its own: L2 bandwidth is what bounds that one.
 //   single  128 x 128 or 128 x 64 tiles, where the pair's would leave SMs idle.
+//   split   a cluster of up to 8 CTAs shares the k of one 128 x 64 tile, where even
+//           those are few and k is long (a narrow layer's weight gradient): the
+//           partial sums are added through distributed shared memory, in rank order.
 // Warps 0 and 3 load A and B by TMA (one k-block of 128 bytes is one 128-byte
 // swizzled row; a TMA instruction holds its thread for hundreds of cycles, so one
 // warp for both could not keep up), warp 2 gathers the scale words of both operands into shared memory, warp
@@ -40,7 +43,7 @@ constexpr int kEpi = 256;                        // epilogue threads
 constexpr int kScaleRing = 4;                    // scale words in flight: 512 of k each
 constexpr int kChunkBlocks = 32;                 // fp32 results: k-blocks per TMEM accumulation
 
-// PAIR: BN is 256, shared by the two CTAs.
+// PAIR: BN is 256, shared by the two CTAs.  SPLIT: one tile per cluster.
 template <int BN, bool PAIR>
 struct BlockCfg {
   static_assert(!PAIR || BN == 256, "a pair computes 256 x 256 tiles");
@@ -73,6 +76,7 @@ struct BlockParams {
   int32_t m, n, k_blocks;
   int32_t dtype, accumulate, wide_store;
   int32_t tiles_m, tiles_n, band;
+  int32_t shares;                                // SPLIT: CTAs per tile
 };
 
 // D[tmem] (+)= (A 2^sa) (B 2^sb)^T over 32 of k, e4m3 operands with E8M0 scales.
@@ -214,7 +218,21 @@ __device__ __forceinline__ void store_row(const BlockParams& p, int row, int col
   }
 }
 
-template <int BN, bool PAIR>
+// One result.
+__device__ __forceinline__ void store_one(const BlockParams& p, int row, int col, float v) {
+  if (row >= p.m || col >= p.n) return;
+  const int64_t at = static_cast<int64_t>(row) * p.ldd + col;
+  if (p.dtype == MUONH_DTYPE_F32) {
+    float* d = static_cast<float*>(p.d) + at;
+    *d = p.accumulate ? *d + v : v;
+  } else if (p.dtype == MUONH_DTYPE_BF16) {
+    static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
+  } else {
+    static_cast<__half*>(p.d)[at] = __float2half_rn(v);
+  }
+}
+
+template <int BN, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     block_matmul_kernel(const __grid_constant__ BlockParams p, const __grid_constant__ CUtensorMap amap,
                         const __grid_constant__ CUtensorMap bmap) {
@@ -232,8 +250,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  static_assert(!SPLIT || (!PAIR && BN == 64), "k is shared over 128 x 64 tiles");
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;   // 0 = leader: issues the MMAs, holds full, sfull and tempty
-  const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
+  // SPLIT: this CTA's k-blocks, in whole scale words; the cluster's tile is its worker number
+  const uint32_t share = SPLIT ? cluster_ctarank() : 0, shares = SPLIT ? p.shares : 1;
+  const int words = (p.k_blocks + 3) / 4;
+  const int k_first = SPLIT ? 4 * static_cast<int>(words * share / shares) : 0;
+  const int k_last = SPLIT ? min(p.k_blocks, 4 * static_cast<int>(words * (share + 1) / shares)) : p.k_blocks;
+  const int worker = SPLIT ? blockIdx.x / shares : blockIdx.x / kCtas;
+  const int workers = SPLIT ? gridDim.x / shares : gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -279,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every role walks over the same (tile, chunk of k) sequence
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int chunk = p.dtype == MUONH_DTYPE_F32 ? kChunkBlocks : p.k_blocks;
+  float sum[SPLIT ? 32 : 1] = {};                // SPLIT: an epilogue thread's part of the tile
 
   if (warp == 0 || warp == 3) {
     if (lane == 0) {
@@ -293,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_at(p, t, tm, tn);
         const int row = role_a ? tm * C::kTileRows + static_cast<int>(rank) * kTm
                                : tn * BN + static_cast<int>(rank) * C::kBRows;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = k_first; kb < k_last; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, err)) {
             ok = false;
             break;
@@ -332,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int64_t t = worker; t < tiles && ok; t += workers) {
         int left = 0;                            // k-blocks until the accumulator is complete
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = k_first; kb < k_last; ++kb) {
           const bool fresh = left == 0;
           if (fresh) {
-            left = min(chunk, p.k_blocks - kb);
+            left = min(chunk, k_last - kb);
             if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, err)) {
               ok = false;
               break;
@@ -389,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage = 0;
             phase ^= 1u;
           }
-          if (((kb & 3) == 3 || kb == p.k_blocks - 1) && ++ring == kScaleRing) {
+          if (((kb & 3) == 3 || kb == k_last - 1) && ++ring == kScaleRing) {
             ring = 0;
             ring_phase ^= 1u;
           }
@@ -427,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows[b][j] = b == 0 ? (row < p.m ? p.sa + static_cast<int64_t>(row >> p.sa_shift) * p.ld_sa : nullptr)
                               : (in_b < BN && row < p.n ? p.sb + static_cast<int64_t>(row >> p.sb_shift) * p.ld_sb : nullptr);
         }
-      for (int w0 = 0; 4 * w0 < p.k_blocks && ok; w0 += kScaleRing) {
+      for (int w0 = k_first / 4; 4 * w0 < k_last && ok; w0 += kScaleRing) {
         // kScaleRing groups at once: their loads are in flight together (one
         // group at a time, the MMAs waited for scales a third of the time)
         uint32_t u[kScaleRing][C::kScaleBlocks][4];
@@ -437,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < C::kScaleBlocks; ++b)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              u[g][b][j] = 4 * (w0 + g) < p.k_blocks
+              u[g][b][j] = 4 * (w0 + g) < k_last
                                ? scale_word(rows[b][j], b == 0 ? p.sa_words : p.sb_words, w0 + g, p.k_blocks)
                                : 0u;
 #pragma unroll
         for (int g = 0; g < kScaleRing; ++g) {
-          if (4 * (w0 + g) >= p.k_blocks) break;
+          if (4 * (w0 + g) >= k_last) break;
           if (!mbar_wait(&sempty[ring], ring_phase ^ 1u, err)) ok = false;
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -475,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(p, t, tm, tn);
       const int row = tm * C::kTileRows + static_cast<int>(rank) * kTm + quarter * 32 + lane;
       const int col = tn * BN + half * kCols;
-      for (int kb = 0; kb < p.k_blocks; kb += chunk) {
+      for (int kb = k_first; kb < k_last; kb += chunk) {
         if (!mbar_wait(&tfull[acc], acc_phase, err)) {
           ok = false;
           break;
@@ -491,11 +517,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc = 0;
           acc_phase ^= 1u;
         }
-        const bool add = kb > 0 || p.accumulate;
+        if constexpr (SPLIT) {
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) store_row(p, row, col + 32 * c, v[c], add);
+          for (int j = 0; j < 32; ++j) sum[j] += v[0][j];
+        } else {
+          const bool add = kb > 0 || p.accumulate;
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) store_row(p, row, col + 32 * c, v[c], add);
+        }
       }
     }
+  }
+
+  if constexpr (SPLIT) {
+    // the operands' space is free (every product is done): each CTA leaves its
+    // sums there, 8 vectors per epilogue thread, and adds up and stores the
+    // vectors whose number modulo the CTAs is its own
+    __syncthreads();
+    float4* const mine = reinterpret_cast<float4*>(smem) + (threadIdx.x - (kThreads - kEpi));
+    if (warp >= 4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        mine[j * kEpi] = make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2], sum[4 * j + 3]);
+    }
+    cluster_sync();
+    if (warp >= 4) {
+      int tm, tn;
+      tile_at(p, worker, tm, tn);
+      const int row = tm * kTm + (warp & 3) * 32 + lane, col = tn * BN + ((warp - 4) >> 2) * (BN / 2);
+      for (int j = share; j < 8; j += shares) {
+        float4 total = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t r = 0; r < shares; ++r) {
+          const float4 v = load_cluster_f4(map_shared_rank(mine + j * kEpi, r));
+          total.x += v.x, total.y += v.y, total.z += v.z, total.w += v.w;
+        }
+        const float out[4] = {total.x, total.y, total.z, total.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_one(p, row, col + 4 * j + i, out[i]);
+      }
+    }
+    cluster_sync();                              // no CTA leaves while another reads its sums
   }
 
   tc_fence_before();
@@ -523,23 +584,24 @@ muonh_status block_fail(muonh_status st, const char* msg) {
   return st;
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool SPLIT>
 cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUtensorMap& b, int workers, cudaStream_t s) {
-  const auto kernel = block_matmul_kernel<BN, PAIR>;
+  const auto kernel = block_matmul_kernel<BN, PAIR, SPLIT>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockCfg<BN, PAIR>::kSmem);
   if (e != cudaSuccess) return e;
+  const unsigned cluster = PAIR ? 2u : SPLIT ? static_cast<unsigned>(p.shares) : 1u;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? 2 * workers : workers));
+  cfg.gridDim = dim3(cluster * static_cast<unsigned>(workers));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = BlockCfg<BN, PAIR>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = PAIR ? 2 : 1;
+  attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p, a, b);
 }
 
@@ -620,9 +682,16 @@ extern "C" muonh_status muonh_block_matmul(const muonh_block_operand* a, const m
   if (!map(&amap, a, kTm) || !map(&bmap, b, pair ? 128 : bn))
     return block_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   const int workers = static_cast<int>(std::min<int64_t>(tiles(rows, bn), pair ? sms / 2 : sms));
-  const cudaError_t e = pair        ? launch_block<256, true>(p, amap, bmap, workers, s)
-                        : bn == 128 ? launch_block<128, false>(p, amap, bmap, workers, s)
-                                    : launch_block<64, false>(p, amap, bmap, workers, s);
+  // few tiles and a long k: up to 8 CTAs per tile, with 512 of k each at least
+  p.shares = 1;
+  // (clusters of 8 have to find 8 free SMs in one GPC: two thirds of the SMs at most)
+  while (bn == 64 && p.shares < 8 && tiles(kTm, 64) * p.shares * 2 <= (p.shares == 4 ? sms * 2 / 3 : sms) &&
+         k_blocks >= 8 * p.shares)
+    p.shares *= 2;
+  const cudaError_t e = pair           ? launch_block<256, true, false>(p, amap, bmap, workers, s)
+                        : bn == 128    ? launch_block<128, false, false>(p, amap, bmap, workers, s)
+                        : p.shares > 1 ? launch_block<64, false, true>(p, amap, bmap, workers, s)
+                                       : launch_block<64, false, false>(p, amap, bmap, workers, s);
   if (e != cudaSuccess) return block_fail(MUONH_ERR_CUDA, "launch of block_matmul_kernel failed");
   return MUONH_OK;
 }

@@ -506,6 +506,15 @@ __device__ __forceinline__ uint32_t map_shared_rank(const void* p, uint32_t rank
   return r;
 }
 
+// 16 bytes at such an address (the callers' cluster barriers order the access).
+__device__ __forceinline__ float4 load_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr));
+  return v;
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -182,15 +182,6 @@ __device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r,
     products<K>(d, k_major(l + (prod == 2 ? kSliceBytes : 0)), mn_major(r + (prod == 1 ? kSliceBytes : 0)), idesc, prod);
 }
 
-// 16 bytes of another CTA's shared memory (the callers' cluster barriers order it).
-__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 // The sum over the cluster's R CTAs of the 32 values of each epilogue thread,
 // which every CTA has left at smem as 8 vectors per thread.  Each CTA adds
 // 8/R of the vectors, in rank order, and then all fetch each other's: 2 x 64
@@ -209,7 +200,7 @@ __device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (
     for (int i = 0; i < R; ++i) {
       const uint32_t from = map_shared_rank(smem, (rank + 1 + i) % R) + at;
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) v[i * kEach + j] = load_cluster(from + (rank * kEach + j) * kEpiThreads * 16);
+      for (int j = 0; j < kEach; ++j) v[i * kEach + j] = load_cluster_f4(from + (rank * kEach + j) * kEpiThreads * 16);
     }
     // v[i] came from CTA (rank + 1 + i) % R: rotated back, so that the sum is in rank order
 #pragma unroll
@@ -238,7 +229,7 @@ __device__ __forceinline__ void add_shares(uint8_t* smem, uint32_t rank, float (
       // the vectors of CTA r are numbers r kEach and on; acc is indexed statically
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
-        const float4 v = load_cluster(from + (r * kEach + j) * kEpiThreads * 16);
+        const float4 v = load_cluster_f4(from + (r * kEach + j) * kEpiThreads * 16);
 #pragma unroll
         for (int s = 0; s < R; ++s)
           if (static_cast<uint32_t>(s) == r) {
@@ -633,16 +624,31 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   if (threadIdx.x == 0 && *err) atomicOr(&g_orth_timeout, 1);
 }
 
-// Copies a stack whose rows TMA cannot address to one whose rows it can, or back.
+// Copies a stack whose rows TMA cannot address to one whose rows it can, or
+// back: `lanes` lanes of a warp per row, element by element.
 __global__ void __launch_bounds__(256)
     copy_stack_kernel(const uint16_t* from, int64_t from_stride, int64_t from_ld, uint16_t* to, int64_t to_stride,
-                      int64_t to_ld, int64_t batch, int64_t rows, int64_t cols) {
-  const int64_t total = batch * rows * cols, step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += step) {
-    const int64_t r = i / cols, c = i - r * cols, b = r / rows;
-    const int64_t y = r - b * rows;
-    to[b * to_stride + y * to_ld + c] = from[b * from_stride + y * from_ld + c];
+                      int64_t to_ld, int64_t batch, int64_t rows, int cols, int lanes) {
+  const int per_block = 256 / lanes, lane = threadIdx.x % lanes;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes; r < batch * rows;
+       r += static_cast<int64_t>(gridDim.x) * per_block) {
+    const int64_t b = r / rows, y = r - b * rows;
+    const uint16_t* src = from + b * from_stride + y * from_ld;
+    uint16_t* dst = to + b * to_stride + y * to_ld;
+#pragma unroll 8
+    for (int c = lane; c < cols; c += lanes) dst[c] = src[c];
   }
+}
+
+cudaError_t copy_stack(const void* from, int64_t from_stride, int64_t from_ld, void* to, int64_t to_stride, int64_t to_ld,
+                       const muonh_orthogonalize_desc& d, int sms, cudaStream_t s) {
+  int lanes = 4;
+  while (lanes < 32 && lanes < d.cols) lanes *= 2;
+  const int64_t blocks = (d.batch * d.rows + 256 / lanes - 1) / (256 / lanes);
+  copy_stack_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sms)), 256, 0, s>>>(
+      static_cast<const uint16_t*>(from), from_stride, from_ld, static_cast<uint16_t*>(to), to_stride, to_ld, d.batch,
+      d.rows, static_cast<int>(d.cols), lanes);
+  return cudaGetLastError();
 }
 
 muonh_status orth_fail(muonh_status st, const char* msg) {
@@ -759,13 +765,12 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
 
-  const int64_t ld = up8(d->cols), copies = std::min<int64_t>((d->batch * d->rows * d->cols + 255) / 256, 16ll * sms);
+  const int64_t ld = up8(d->cols);
   Stack in{const_cast<void*>(d->x), d->x_stride, d->ldx}, out{d->out, d->out_stride, d->ldo};
   uint8_t* work = static_cast<uint8_t*>(workspace);
   if (!tma_stack(in.p, in.stride, in.ld, d->batch, d->rows)) {
-    copy_stack_kernel<<<static_cast<unsigned>(copies), 256, 0, s>>>(
-        static_cast<const uint16_t*>(in.p), in.stride, in.ld, reinterpret_cast<uint16_t*>(work), ld * d->rows, ld,
-        d->batch, d->rows, d->cols);
+    if (copy_stack(in.p, in.stride, in.ld, work, ld * d->rows, ld, *d, sms, s) != cudaSuccess)
+      return orth_fail(MUONH_ERR_CUDA, "launch of copy_stack_kernel failed");
     in = Stack{work, ld * d->rows, ld};
     work += copy_bytes(*d);
   }
@@ -809,12 +814,7 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   if (e == cudaSuccess)
     e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
              : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);
-  if (e == cudaSuccess && copy_back) {
-    copy_stack_kernel<<<static_cast<unsigned>(copies), 256, 0, s>>>(
-        static_cast<const uint16_t*>(out.p), out.stride, out.ld, static_cast<uint16_t*>(d->out), d->out_stride, d->ldo,
-        d->batch, d->rows, d->cols);
-  }
-  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess && copy_back) e = copy_stack(out.p, out.stride, out.ld, d->out, d->out_stride, d->ldo, *d, sms, s);
   if (e != cudaSuccess) return orth_fail(MUONH_ERR_CUDA, "launch of the orthogonalize kernel failed");
   return MUONH_OK;
 }

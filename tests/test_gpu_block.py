@@ -133,7 +133,8 @@ def _operand(rng, rows, k, block_rows):
 
 
 PRODUCTS = [(1, 1, 1), (1, 64, 128), (3, 7, 33), (128, 128, 128), (130, 70, 260), (77, 520, 1000), (128, 256, 512),
-            (300, 257, 640), (64, 2048, 896), (2500, 1900, 400), (3000, 2700, 1160)]
+            (300, 257, 640), (64, 2048, 896), (2500, 1900, 400), (3000, 2700, 1160),
+            (100, 200, 9000), (5, 3, 1024), (260, 70, 5000)]
 
 
 @pytest.mark.parametrize("blocks", [(1, 1), (1, 128), (128, 1), (128, 128)])
