@@ -22,9 +22,14 @@
 // rank order, and every CTA then runs the same r x r iteration: with few
 // matrices the SMs would otherwise be idle, with many the cluster is one CTA.
 //
-// What bounds it.  The r x r iteration is a chain of 14 dependent products of 24
-// MMAs (128 x 128 x 16) with a pass of the epilogue between them: 55 of the 70 us
-// a lone matrix [128, 2048] takes at 8 CTAs... see kLateNs for many of them.
+// What bounds it, for one [128, 2048] bf16 matrix on each of 148 SMs (119k
+// cycles, 76 us): X X^T 28k cycles, reading 78 MB from HBM; the r x r iteration
+// 50k, a chain of 14 dependent products of 24 MMAs (128 x 128 x 16, 2k cycles
+// each with their hand-over) and as many passes of the epilogue (1.0 to 1.4k,
+// bound by its instructions: 512 threads, so 96 registers each); Q X 29k, 1.5k
+// per slice: its operands' reads, the slice's arrival and its result's way out
+// share the 128 bytes per cycle of shared memory.  The chain is what a single
+// matrix costs whatever its long side.
 //
 // Precision.  The products are 16-bit with fp32 accumulation.  X X^T is exact
 // up to the accumulation: X is used as it is.  The r x r operands are kept as
