@@ -355,7 +355,9 @@ muonh_status muonh_adamw_step(const muonh_adamw_tensor* tensors, int32_t n, cons
 
 /* ---------------------------------------------------------------------------
  * Operators around the update: the layers whose gradients the optimizers
- * read.  Stateless; enqueued on `stream`; scratch is the caller's.
+ * read.  Stateless; enqueued on `stream`; scratch is the caller's.  Results
+ * are the same bit for bit for the same inputs on the same kind of device.
+ * A first call on a device loads its kernels: make it before capturing one.
  * ------------------------------------------------------------------------- */
 
 /* Layer norm of `rows` rows of n elements, and the RMS norm of a
@@ -405,8 +407,9 @@ muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void*
  *   ns_steps    0 .. 16;  eps >= 0 (a matrix of zeros gives zeros).
  * The result is off by the rounding to its type and, for an ill-conditioned X,
  * up to about 1e-3 of ||out|| (the r x r iterates are kept to 22 bits).
- * ||X||_F^2 is held in fp32, so norms must be below 1.8e19; a matrix that holds
- * NaN or Inf gives NaN throughout and leaves the others alone.
+ * ||X||_F^2 is held in fp32, so norms must be below 1.8e19, and one below 1e-19
+ * counts as zero; a matrix that holds NaN or Inf gives NaN throughout and leaves
+ * the others alone.
  *   workspace   16-byte aligned device scratch of muonh_orthogonalize_workspace
  *               bytes: 0 where base pointers and strides are multiples of 16
  *               bytes, else room for a copy of the stacks that are not.

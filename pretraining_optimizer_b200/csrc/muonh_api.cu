@@ -202,16 +202,14 @@ void muonh::ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, i
   struct Memo {
     float a, b, c;
     int steps = -1;
-    int32_t ea, eb;
-    std::vector<int32_t> eq;
+    int32_t ea, eb, eq[kMaxChainSteps];
   };
   static thread_local Memo memo;
   if (memo.steps != steps || memo.a != a || memo.b != b || memo.c != c) {
     int32_t ex, ec;
     scale_exponents(a, b, c, steps, P_FP16, &ex, &memo.ea, &ec, &memo.eb);
     const double smax = iterate_bound(a, b, c, steps);
-    memo.eq.clear();
-    for (int k = 0; k < steps; ++k) memo.eq.push_back(q_exponent(a, b, c, k + 1, smax));
+    for (int k = 0; k < steps; ++k) memo.eq[k] = q_exponent(a, b, c, k + 1, smax);
     memo.a = a;
     memo.b = b;
     memo.c = c;
@@ -219,7 +217,7 @@ void muonh::ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, i
   }
   *ea = memo.ea;
   *eb = memo.eb;
-  std::copy(memo.eq.begin(), memo.eq.end(), eq);
+  std::copy(memo.eq, memo.eq + steps, eq);
 }
 
 bool muonh::encode_tiled_stack(CUtensorMap* out, void* base, bool bf16, int64_t cols, int64_t rows, int64_t batch,

@@ -457,7 +457,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int ab_bf16, int 
 
 // Power-of-two scales of the fp16 operands of a Newton-Schulz run on r x r
 // matrices: of A (and A p(A)), of p(A), and of the product of the first k + 1
-// factors p(A_0) ... p(A_k) in eq[k].
+// factors p(A_0) ... p(A_k) in eq[k], for at most kMaxChainSteps steps.
+constexpr int kMaxChainSteps = 16;
 void ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq);
 
 // 3-D map over a stack of 16-bit matrices (`batch` of rows x cols, row stride

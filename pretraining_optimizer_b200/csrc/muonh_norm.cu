@@ -532,13 +532,13 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_forward_ring_kernel(cons
 #pragma unroll
       for (int i = 0; i < V; ++i) v[k * V + i] = 0.f;
       if (j < n) read_row<T, V>(x + j, v + k * V);
-#pragma unroll
-      for (int i = 0; i < V; ++i) mu += v[k * V + i];
     }
-    // (the RMS norm needs this barrier too: the slot has been read after it)
-    total(mu);
-    mu = p.mean ? mu * inv_n : 0.f;
-    if (t == 0 && row + ring.ring * step < p.rows) ring.fill(slot, row + ring.ring * step);
+    if (p.mean) {
+#pragma unroll
+      for (int i = 0; i < P * V; ++i) mu += v[i];
+      total(mu);
+      mu *= inv_n;
+    }
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       if ((k * G + t) * V < n) {
@@ -550,6 +550,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_forward_ring_kernel(cons
       }
     }
     total(q);
+    // every thread has read the slot before that barrier
+    if (t == 0 && row + ring.ring * step < p.rows) ring.fill(slot, row + ring.ring * step);
     const float rstd = rsqrtf(fmaf(q, inv_n, p.eps));
     T* y = static_cast<T*>(p.out) + row * p.ldo;
 #pragma unroll

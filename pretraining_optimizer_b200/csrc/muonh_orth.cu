@@ -62,7 +62,7 @@ static_assert(kOrthSmem <= 227 * 1024, "shared memory of the orthogonalize kerne
 constexpr int kEpiThreads = 512;                  // 16 epilogue warps: 32 rows x 32 columns each
 constexpr int kOrthThreads = 64 + kEpiThreads;    // warp 0 TMA, warp 1 MMA
 constexpr int kGramChunk = 16;                    // slices (2048 columns) per TMEM accumulation
-constexpr int kMaxSteps = 16;
+constexpr int kMaxSteps = kMaxChainSteps;
 // With several matrices per SM all SMs read X, iterate and write at the same
 // time, and HBM idles during the r x r iterations.  Half of the SMs start a
 // quarter of a matrix later: 896 x [128, 2048] took 437 us without, 403 with 15
