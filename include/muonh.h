@@ -357,7 +357,9 @@ muonh_status muonh_adamw_step(const muonh_adamw_tensor* tensors, int32_t n, cons
  * Operators around the update: the layers whose gradients the optimizers
  * read.  Stateless; enqueued on `stream`; scratch is the caller's.  Results
  * are the same bit for bit for the same inputs on the same kind of device.
- * A first call on a device loads its kernels: make it before capturing one.
+ * A first call on a device loads its kernels and raises their shared memory:
+ * make it before capturing one, with the primary context current, and make
+ * none after cudaDeviceReset.
  * ------------------------------------------------------------------------- */
 
 /* Layer norm of `rows` rows of n elements, and the RMS norm of a

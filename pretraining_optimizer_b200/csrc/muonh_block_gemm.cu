@@ -587,8 +587,8 @@ muonh_status block_fail(muonh_status st, const char* msg) {
 template <int BN, bool PAIR, bool SPLIT>
 cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUtensorMap& b, int workers, cudaStream_t s) {
   const auto kernel = block_matmul_kernel<BN, PAIR, SPLIT>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BlockCfg<BN, PAIR>::kSmem);
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = allow_shared(kernel, done, BlockCfg<BN, PAIR>::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned cluster = PAIR ? 2u : SPLIT ? static_cast<unsigned>(p.shares) : 1u;
   cudaLaunchConfig_t cfg{};

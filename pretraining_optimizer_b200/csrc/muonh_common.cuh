@@ -9,6 +9,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/muonh.h"
 
 namespace muonh {
@@ -572,6 +574,21 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 }
 
 // --------------------------------------------------------- launch helpers
+// Lets `kernel` use up to `bytes` of dynamic shared memory on the current device.
+// `done` (one per kernel) remembers the devices that know: the call takes about a
+// microsecond, a tenth of the smallest operator calls.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, std::atomic<uint64_t>& done, int bytes) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (set == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return set;
+}
+
 cudaError_t launch_ns_gemm(int mode, int prec, const NsParams& p, int grid, cudaStream_t s);
 cudaError_t launch_ns_gemm_pair(int mode, int prec, const NsParams& p, int pairs, cudaStream_t s);
 size_t ns_gemm_smem_bytes(int prec);

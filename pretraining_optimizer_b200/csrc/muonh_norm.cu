@@ -37,6 +37,7 @@ constexpr int kMaxPack = 16;                        // elements of a row per thr
 constexpr int kWide = kNormThreads * kMaxPack;      // widest row held in registers: 8192
 constexpr int kMaxParts = 512;                      // partial rows of dw/db
 constexpr int kMaxRing = 4;                         // rows in flight per group
+constexpr int kMaxShared = 227 * 1024;
 
 __device__ int g_norm_timeout;                      // a wait gave up in some call since the flag was read
 
@@ -733,6 +734,8 @@ constexpr int kJoinSlices = 16;
 __global__ void __launch_bounds__(32 * kJoinSlices)
     norm_join_kernel(const float* part_w, const float* part_b, float* dw, float* db, int parts, int n) {
   __shared__ float s[kJoinSlices][33];
+  // launched while the kernel that writes the partial rows still runs
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* part = blockIdx.y ? part_b : part_w;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
@@ -806,7 +809,8 @@ cudaError_t launch_ring(const NormParams& p, Pass pass, int grid, size_t smem, c
   void (*kernel)(NormParams) = pass == kForward    ? norm_forward_ring_kernel<T, V, P, G>
                                : pass == kBackward ? norm_backward_ring_kernel<T, V, P, G, true>
                                                    : norm_backward_ring_kernel<T, V, P, G, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> done[3];
+  const cudaError_t e = allow_shared(kernel, done[pass], kMaxShared);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kNormThreads, smem, s>>>(p);
   return cudaGetLastError();
@@ -1032,9 +1036,17 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
     e = launch(p, dtype, sums ? kBackward : kBackwardRows, vec, elems, grid, smem, s);
   }
   if (e == cudaSuccess && sums && parts > 1) {
-    norm_join_kernel<<<dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1), 32 * kJoinSlices, 0, s>>>(
-        p.part_w, p.part_b, dweight, dbias, parts, p.n);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1);
+    cfg.blockDim = dim3(32 * kJoinSlices);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, norm_join_kernel, static_cast<const float*>(p.part_w),
+                           static_cast<const float*>(p.part_b), dweight, dbias, parts, p.n);
   }
   if (e != cudaSuccess) return norm_fail(MUONH_ERR_CUDA, "launch of a layer norm backward kernel failed");
   return MUONH_OK;

@@ -41,7 +41,6 @@
 // accumulated in TMEM before they are added in IEEE fp32 registers.
 // The result is rounded once to X's type.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "muonh_common.cuh"
@@ -799,10 +798,10 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   if (!encode_stack(&xmap, in, *d, kSide) || !encode_stack(&omap, out, *d, 32))
     return orth_fail(MUONH_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   const bool bf16 = d->dtype == MUONH_DTYPE_BF16;
-  cudaError_t e = bf16 ? cudaFuncSetAttribute(orthogonalize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kOrthSmem)
-                       : cudaFuncSetAttribute(orthogonalize_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kOrthSmem);
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = bf16 ? allow_shared(orthogonalize_kernel<true>, done[1], kOrthSmem)
+                       : allow_shared(orthogonalize_kernel<false>, done[0], kOrthSmem);
+  if (e != cudaSuccess) return orth_fail(MUONH_ERR_CUDA, "the kernel's shared memory was refused");
   const int ranks = pick_cluster(bf16, d->batch, p.slices, dev);
   p.late_below = d->batch >= static_cast<int64_t>(kLateWaves) * sms ? sms : 0;
   cudaLaunchConfig_t cfg{};
@@ -816,9 +815,8 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (e == cudaSuccess)
-    e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
-             : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);
+  e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
+           : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);
   if (e == cudaSuccess && copy_back) e = copy_stack(out.p, out.stride, out.ld, d->out, d->out_stride, d->ldo, *d, sms, s);
   if (e != cudaSuccess) return orth_fail(MUONH_ERR_CUDA, "launch of the orthogonalize kernel failed");
   return MUONH_OK;
