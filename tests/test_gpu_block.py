@@ -134,7 +134,7 @@ def _operand(rng, rows, k, block_rows):
 
 PRODUCTS = [(1, 1, 1), (1, 64, 128), (3, 7, 33), (128, 128, 128), (130, 70, 260), (77, 520, 1000), (128, 256, 512),
             (300, 257, 640), (64, 2048, 896), (2500, 1900, 400), (3000, 2700, 1160),
-            (100, 200, 9000), (5, 3, 1024), (260, 70, 5000)]
+            (100, 200, 9000), (5, 3, 1024), (260, 70, 5000), (2300, 2310, 4300), (256, 256, 128), (1700, 1500, 136)]
 
 
 @pytest.mark.parametrize("blocks", [(1, 1), (1, 128), (128, 1), (128, 128)])
@@ -280,3 +280,46 @@ def test_the_same_bits_on_any_stream_and_in_a_graph():
     t.cuda.synchronize()
     assert t.equal(got, layer())
     operator_status()
+
+
+def test_an_operand_with_itself_and_results_that_alternate():
+    """The same operand on both sides, and calls that follow each other without a wait."""
+    t = _t()
+    from pretraining_optimizer_b200 import block_matmul
+    rng = np.random.default_rng(8)
+    a, sa = _operand(rng, 300, 700, 1)
+    va = O.block_values(a.float().cpu().numpy(), sa.cpu().numpy())
+    b, sb = _operand(rng, 2100, 700, 128)
+    vb = O.block_values(b.float().cpu().numpy(), sb.cpu().numpy())
+    results = []
+    for _ in range(5):
+        results.append((block_matmul(a, sa, a, sa, dtype=t.float32), block_matmul(b, sb, b, sb, dtype=t.float32)))
+    for small, large in results:
+        assert np.array_equal(_np(small), va @ va.T) and np.array_equal(_np(large), vb @ vb.T)
+
+
+def test_refusals_of_the_binding():
+    t = _t()
+    from pretraining_optimizer_b200 import MuonHError, block_matmul, block_quantize
+    q, s = block_quantize(t.ones(40, 200, device="cuda:0"))
+    r, rs = block_quantize(t.ones(30, 200, device="cuda:0"))
+    with pytest.raises(ValueError):
+        block_matmul(q, s[:, :1], r, rs)                      # too few scales
+    with pytest.raises(ValueError):
+        block_matmul(q, s[:7], r, rs)
+    with pytest.raises(ValueError):
+        block_matmul(q[:, :128], s[:, :1], r, rs)             # different k
+    with pytest.raises(MuonHError):
+        block_matmul(q.contiguous(), s, r, rs)                # rows of 200 bytes: not 16-byte aligned
+    with pytest.raises(TypeError):
+        block_matmul(q, s, r, rs, dtype=t.float64)
+    with pytest.raises(ValueError):
+        block_matmul(q, s, r, rs, accumulate=True)            # nothing to add to
+    with pytest.raises(MuonHError):
+        block_matmul(q, s, r, rs, out=t.zeros(40, 30, dtype=t.bfloat16, device="cuda:0"), accumulate=True)
+    with pytest.raises(ValueError):
+        block_matmul(q, s, r, rs, out=t.zeros(30, 40, device="cuda:0"))
+    with pytest.raises(ValueError):
+        block_quantize(t.ones(4, 8, 8, device="cuda:0"))
+    with pytest.raises(ValueError):
+        block_quantize(t.ones(8, 8, device="cuda:0").t()[:, ::2])

@@ -251,3 +251,61 @@ def test_captured_in_a_graph():
     want, m2, r2 = layer_norm(x2, w, b)
     want_grads = layer_norm_backward(dy2, x2, w, m2, r2, bias=True)
     assert t.equal(y, want) and all(t.equal(a, c) for a, c in zip(grads, want_grads))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [64, 65, 256, 257, 512, 513, 520, 1024, 1028, 2047, 2048, 2052, 4096, 4097, 4100, 8190])
+def test_widths_around_the_kernels_borders(n, dtype):
+    """Both sides of every change of kernel and of threads per row, with more rows than groups of threads."""
+    from pretraining_optimizer_b200 import layer_norm, layer_norm_backward
+    rows = 1400 if n <= 4096 else 700
+    x, dy, w, b = _data(rows, n, _dtype(dtype), seed=n)
+    y, mean, rstd = layer_norm(x, w, b, eps=1e-6)
+    check_forward(x, w, b, 1e-6, False, y, mean, rstd)
+    check_backward(dy, x, w, mean, rstd, *layer_norm_backward(dy, x, w, mean, rstd, bias=True))
+
+
+@pytest.mark.parametrize("n", [100, 777, 3000])
+def test_each_combination_of_gradients(n):
+    t = _t()
+    from pretraining_optimizer_b200 import layer_norm, layer_norm_backward
+    x, dy, w, _ = _data(333, n, t.bfloat16)
+    _, mean, rstd = layer_norm(x, w)
+    dx, dw, db = layer_norm_backward(dy, x, w, mean, rstd, bias=True)
+    alone, dw2, none = layer_norm_backward(dy, x, w, mean, rstd)
+    assert none is None and t.equal(alone, dx) and t.equal(dw2, dw)
+    plain, none, db2 = layer_norm_backward(dy, x, None, mean, rstd, bias=True)
+    assert none is None and t.equal(db2, db)
+    check_backward(dy, x, None, mean, rstd, plain, None, db2)
+    rows_only = layer_norm_backward(dy, x, None, mean, rstd)
+    assert rows_only[1:] == (None, None) and t.equal(rows_only[0], plain)
+
+
+@pytest.mark.parametrize("n", [127, 1001, 5003, 9001])
+def test_unaligned_rows_in_place(n):
+    """Neighbouring rows share 16-byte pieces; writing a row leaves the others as they are."""
+    t = _t()
+    from pretraining_optimizer_b200 import layer_norm
+    x, _, w, b = _data(900, n, t.bfloat16)
+    ref, _, _ = layer_norm(x, w, b)
+    got, _, _ = layer_norm(x, w, b, out=x)
+    assert got is x and t.equal(x, ref)
+
+
+def test_on_a_side_stream_after_its_own_work():
+    """A call on a stream sees what that stream did before, and its results belong to it."""
+    t = _t()
+    from pretraining_optimizer_b200 import layer_norm, layer_norm_backward
+    x, dy, w, b = _data(4000, 1024, t.bfloat16)
+    want = layer_norm_backward(dy, x, w, *layer_norm(x, w, b)[1:], bias=True)
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        late = t.zeros_like(x)
+        for _ in range(20):
+            late.mul_(2.0)
+        late.copy_(x)
+    y, mean, rstd = layer_norm(late, w, b, stream=side)
+    got = layer_norm_backward(dy, late, w, mean, rstd, bias=True, stream=side)
+    side.synchronize()
+    assert all(t.equal(a, c) for a, c in zip(want, got))

@@ -249,3 +249,37 @@ def test_agrees_with_the_step_on_one_head():
     opt.close()
     got = orthogonalize(g).double()
     assert float((got - step).norm() / step.norm()) <= 1e-2 + 2.0 ** -8
+
+
+@pytest.mark.parametrize("shape", [(700, 16, 40), (600, 100, 130), (40, 128, 512), (20, 64, 1024), (70, 600, 65), (1, 16, 41000),
+                                   (1, 41000, 16), (2, 128, 5000)])
+def test_stacks_of_every_size(shape):
+    """Several matrices per SM (with the late start), clusters of 2, 4 and 8, and long sides of many accumulations."""
+    t = _t()
+    from pretraining_optimizer_b200 import operator_status, orthogonalize
+    x = t.from_numpy(_spectrum(np.random.default_rng(14), *shape, "plain")).to("cuda:0", t.bfloat16)
+    check(x, orthogonalize(x))
+    operator_status()
+
+
+def test_refusals_of_the_binding():
+    t = _t()
+    from pretraining_optimizer_b200 import MuonHError, orthogonalize
+    x = t.zeros(2, 130, 200, dtype=t.bfloat16, device="cuda:0")
+    with pytest.raises(MuonHError, match="128"):
+        orthogonalize(x)
+    x = x[:, :8]
+    with pytest.raises(TypeError):
+        orthogonalize(x.float())
+    with pytest.raises(ValueError):
+        orthogonalize(x[None])
+    with pytest.raises(ValueError):
+        orthogonalize(x.mT)
+    with pytest.raises(ValueError):
+        orthogonalize(x, out=t.zeros(2, 8, 199, dtype=t.bfloat16, device="cuda:0"))
+    with pytest.raises(TypeError):
+        orthogonalize(x, out=t.zeros(2, 8, 200, dtype=t.float16, device="cuda:0"))
+    with pytest.raises(ValueError):
+        orthogonalize(x, out=x[:1].expand(2, 8, 200))
+    with pytest.raises(MuonHError):
+        orthogonalize(x, ns_steps=17)
