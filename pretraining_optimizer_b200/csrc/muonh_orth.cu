@@ -64,7 +64,7 @@ constexpr int kGramChunk = 16;                    // slices (2048 columns) per T
 constexpr int kMaxSteps = kMaxChainSteps;
 // With several matrices per SM all SMs read X, iterate and write at the same
 // time, and HBM idles during the r x r iterations.  Half of the SMs start a
-// quarter of a matrix later: 896 x [128, 2048] took 437 us without, 403 with 15
+// quarter of a matrix later: 896 x [128, 2048] took 437 us without, 399 with 15
 // us, 406 with 25 us; below four matrices per SM the delay costs what it gives.
 constexpr int kLateNs = 15000;
 constexpr int kLateWaves = 4;
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       if (i >= kRing && !mbar_wait(&e[slot], (i / kRing - 1) & 1, err)) break;
       mbar_expect_tx(&f[slot], kSliceBytes);
       uint8_t* dst = smem + slot * kSliceBytes;
-      const int at = (first + i) * kSide;
+      // the second walk runs backwards: the last slices read are the likeliest to be in L2 still
+      const int at = (first + (pass == 0 ? i : count - 1 - i)) * kSide;
       for (int h = 0; h < 2; ++h)
         load_box(dst + h * kChunkBytes, &xmap, &f[slot], p.tall ? 64 * h : at + 64 * h, p.tall ? at : 0, matrix,
                  policy);
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       fence_proxy_async_smem();
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       if (store) {
-        const int at = (first + i) * kSide;
+        const int at = (first + count - 1 - i) * kSide;
         const int x0 = p.tall ? col0 : at + col0, y0 = p.tall ? at + quarter * 32 : quarter * 32;
         if (x0 < p.cols && y0 < p.rows) store_box(&omap, box + quarter * 4096, x0, y0, matrix, policy);
         bulk_commit();
