@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (PAIR) cluster_sync();                      // barriers initialised in both CTAs
   tc_fence_after();
+  wait_for_stream();
   const uint32_t tmem = *tmem_slot;
   auto arrive_leader = [&](uint64_t* bar) {
     if (PAIR)
@@ -596,12 +597,9 @@ cudaError_t launch_block(const BlockParams& p, const CUtensorMap& a, const CUten
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = BlockCfg<BN, PAIR>::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2] = {programmatic_launch(), cluster_launch(cluster)};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, a, b);
 }
 

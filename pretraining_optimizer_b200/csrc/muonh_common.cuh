@@ -573,7 +573,25 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// Waits until the kernels before this one in the stream are complete and their
+// writes visible.  A kernel launched with the programmatic attribute (below) is
+// set up while they still run, and touches no global memory before this.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // --------------------------------------------------------- launch helpers
+inline cudaLaunchAttribute programmatic_launch() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+inline cudaLaunchAttribute cluster_launch(unsigned ctas) {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = ctas;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  return a;
+}
 // Lets `kernel` use up to `bytes` of dynamic shared memory on the current device.
 // `done` (one per kernel) remembers the devices that know: the call takes about a
 // microsecond, a tenth of the smallest operator calls.

@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(32 * kJoinSlices)
     norm_join_kernel(const float* part_w, const float* part_b, float* dw, float* db, int parts, int n) {
   __shared__ float s[kJoinSlices][33];
   // launched while the kernel that writes the partial rows still runs
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const float* part = blockIdx.y ? part_b : part_w;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
@@ -1040,9 +1040,7 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
     cfg.gridDim = dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1);
     cfg.blockDim = dim3(32 * kJoinSlices);
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr = programmatic_launch();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, norm_join_kernel, static_cast<const float*>(p.part_w),

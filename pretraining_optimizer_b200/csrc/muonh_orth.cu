@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_stream();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_d = tmem + 256, tm_q = tmem + 384;   // r x r products; slice products use columns 0 .. 255
 
@@ -714,10 +715,7 @@ int clusters_at_once(bool bf16, int ranks, int dev) {
   cfg.gridDim = dim3(static_cast<unsigned>(ranks));
   cfg.blockDim = dim3(kOrthThreads);
   cfg.dynamicSmemBytes = kOrthSmem;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr = cluster_launch(static_cast<unsigned>(ranks));
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
@@ -810,12 +808,9 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   cfg.blockDim = dim3(kOrthThreads);
   cfg.dynamicSmemBytes = kOrthSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(ranks);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {cluster_launch(static_cast<unsigned>(ranks)), programmatic_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   e = bf16 ? cudaLaunchKernelEx(&cfg, orthogonalize_kernel<true>, p, xmap, omap)
            : cudaLaunchKernelEx(&cfg, orthogonalize_kernel<false>, p, xmap, omap);
   if (e == cudaSuccess && copy_back) e = copy_stack(out.p, out.stride, out.ld, d->out, d->out_stride, d->ldo, *d, sms, s);
