@@ -148,6 +148,7 @@ __device__ __forceinline__ uint2 quantize_row(const Piece<T>& v, float f) {
 // Groups of 128 along the rows alone; groups are numbered row by row.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) block_quantize_rows_kernel(const __grid_constant__ QuantParams p) {
+  wait_for_stream();
   const uint32_t per_row = static_cast<uint32_t>((p.cols + kTile - 1) / kTile);
   const uint32_t total = static_cast<uint32_t>(p.rows) * per_row;   // below 2^31
   const uint32_t first = blockIdx.x * (kRowsPerThread * kQuantThreads / 16) + (threadIdx.x >> 4);
@@ -207,6 +208,7 @@ __device__ __forceinline__ uint32_t row_maxima(const uint32_t (&m)[8]) {
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
     block_quantize_kernel(const __grid_constant__ QuantParams p) {
+  wait_for_stream();
   constexpr int kWords = Piece<T>::kWords;
   constexpr int kColumnWords = kTile / 8 * kWords;   // a row of the tile
   __shared__ uint32_t column_max[kQuantThreads / 32][kColumnWords];
@@ -328,15 +330,15 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 3 : 2)
 }
 
 template <typename T>
-void launch_quantize(const QuantParams& p, int64_t row_groups, int64_t col_groups, cudaStream_t s) {
+cudaError_t launch_quantize(const QuantParams& p, int64_t row_groups, int64_t col_groups, cudaStream_t s) {
   if (!p.whole && !p.qt) {
     const int64_t groups = p.rows * col_groups, per_block = kRowsPerThread * kQuantThreads / 16;
-    const unsigned grid = static_cast<unsigned>((groups + per_block - 1) / per_block);
-    block_quantize_rows_kernel<T><<<grid, kQuantThreads, 0, s>>>(p);
-    return;
+    return launch_programmatic(block_quantize_rows_kernel<T>, dim3(static_cast<unsigned>((groups + per_block - 1) / per_block)),
+                               kQuantThreads, 0, s, p);
   }
-  const dim3 grid(static_cast<unsigned>(col_groups), static_cast<unsigned>(row_groups));
-  block_quantize_kernel<T><<<grid, kQuantThreads, 0, s>>>(p);
+  return launch_programmatic(block_quantize_kernel<T>,
+                             dim3(static_cast<unsigned>(col_groups), static_cast<unsigned>(row_groups)), kQuantThreads, 0,
+                             s, p);
 }
 
 muonh_status quant_fail(muonh_status st, const char* msg) {
@@ -387,12 +389,9 @@ extern "C" muonh_status muonh_block_quantize(const void* x, int64_t ldx, int64_t
   p.whole = block_rows == kTile;
   p.vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (rows == 1 || ldx * size % 16 == 0) && cols % 8 == 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == MUONH_DTYPE_F32)
-    launch_quantize<float>(p, row_groups, col_groups, s);
-  else if (dtype == MUONH_DTYPE_BF16)
-    launch_quantize<__nv_bfloat16>(p, row_groups, col_groups, s);
-  else
-    launch_quantize<__half>(p, row_groups, col_groups, s);
-  if (cudaGetLastError() != cudaSuccess) return quant_fail(MUONH_ERR_CUDA, "launch of block_quantize_kernel failed");
+  const cudaError_t e = dtype == MUONH_DTYPE_F32    ? launch_quantize<float>(p, row_groups, col_groups, s)
+                        : dtype == MUONH_DTYPE_BF16 ? launch_quantize<__nv_bfloat16>(p, row_groups, col_groups, s)
+                                                    : launch_quantize<__half>(p, row_groups, col_groups, s);
+  if (e != cudaSuccess) return quant_fail(MUONH_ERR_CUDA, "launch of block_quantize_kernel failed");
   return MUONH_OK;
 }

@@ -585,6 +585,20 @@ inline cudaLaunchAttribute programmatic_launch() {
   a.val.programmaticStreamSerializationAllowed = 1;
   return a;
 }
+// A kernel whose first statement is wait_for_stream().
+template <typename... Params, typename... Args>
+cudaError_t launch_programmatic(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                Args&&... args) {
+  cudaLaunchAttribute attr = programmatic_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 inline cudaLaunchAttribute cluster_launch(unsigned ctas) {
   cudaLaunchAttribute a{};
   a.id = cudaLaunchAttributeClusterDimension;

@@ -230,6 +230,7 @@ constexpr int kSumSlots = 2 * kNormThreads / 32;
 
 template <typename T, int V, int P>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_forward_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
   const float inv_n = 1.f / n;
@@ -338,6 +339,7 @@ __device__ __forceinline__ void write_parts(const NormParams& p, int G, float* j
 // SUMS: also the partial rows of dw and db.
 template <typename T, int V, int P, bool SUMS>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   extern __shared__ float joined[];   // [kNormThreads / G][n]: at most kWide floats, 32 KB
   const int G = p.group, t = threadIdx.x % G, n = p.n;
   const int per_block = kNormThreads / G;
@@ -511,6 +513,7 @@ __device__ __forceinline__ RowRing<T, kOperands, G> start_ring(const NormParams&
 
 template <typename T, int V, int P, int G>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_forward_ring_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int per_block = kNormThreads / G;
   const int t = threadIdx.x % G, n = p.n;
@@ -581,6 +584,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_forward_ring_kernel(cons
 
 template <typename T, int V, int P, int G, bool SUMS>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_ring_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int per_block = kNormThreads / G;
   const int t = threadIdx.x % G, n = p.n;
@@ -659,6 +663,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_ring_kernel(con
 // Rows wider than kWide: one block per row, three (two) walks over it.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_forward_wide_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   __shared__ __align__(16) float2 sums[kSumSlots];
   GroupSum<kNormThreads> total(sums);
   const float inv_n = 1.f / p.n;
@@ -688,6 +693,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_wide_kernel(const _
 
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   __shared__ __align__(16) float2 sums[kSumSlots];
   GroupSum<kNormThreads> total(sums);
   const float inv_n = 1.f / p.n;
@@ -714,6 +720,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
 // Partial rows of dw and db, a thread per column and blockIdx.y-th slice of the rows.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant__ NormParams p) {
+  wait_for_stream();
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (j >= p.n) return;
   const int64_t first = p.rows * blockIdx.y / gridDim.y, last = p.rows * (blockIdx.y + 1) / gridDim.y;
@@ -796,12 +803,13 @@ enum Pass { kForward, kBackward, kBackwardRows };   // kBackwardRows: dx alone
 template <typename T, int V, int P>
 cudaError_t launch_row(const NormParams& p, Pass pass, int grid, size_t smem, cudaStream_t s) {
   if (pass == kForward) {
-    if constexpr (V * P <= 8) norm_forward_kernel<T, V, P><<<grid, kNormThreads, 0, s>>>(p);   // at most 8 elements
-  } else if (pass == kBackward)
-    norm_backward_kernel<T, V, P, true><<<grid, kNormThreads, smem, s>>>(p);
-  else
-    norm_backward_kernel<T, V, P, false><<<grid, kNormThreads, 0, s>>>(p);
-  return cudaGetLastError();
+    if constexpr (V * P <= 8)   // the forward pass has at most 8 elements per thread here
+      return launch_programmatic(norm_forward_kernel<T, V, P>, dim3(grid), kNormThreads, 0, s, p);
+    return cudaErrorInvalidValue;
+  }
+  return pass == kBackward
+             ? launch_programmatic(norm_backward_kernel<T, V, P, true>, dim3(grid), kNormThreads, smem, s, p)
+             : launch_programmatic(norm_backward_kernel<T, V, P, false>, dim3(grid), kNormThreads, 0, s, p);
 }
 
 template <typename T, int V, int P, int G>
@@ -812,8 +820,7 @@ cudaError_t launch_ring(const NormParams& p, Pass pass, int grid, size_t smem, c
   static std::atomic<uint64_t> done[3];
   const cudaError_t e = allow_shared(kernel, done[pass], kMaxShared);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kNormThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_programmatic(kernel, dim3(grid), kNormThreads, smem, s, p);
 }
 
 // 128 or 512 threads per row, with 8 or 16 elements each.  The group's size is
@@ -865,22 +872,16 @@ size_t size_ring(NormParams* p, int operands, int size, size_t budget) {
 // Partial rows of dw and db from x and dy: a thread per column, `slices` shares of the rows.
 cudaError_t launch_columns(const NormParams& p, int32_t dtype, int slices, cudaStream_t s) {
   const dim3 grid((p.n + 255) / 256, slices);
-  if (dtype == MUONH_DTYPE_F32)
-    norm_columns_kernel<float><<<grid, 256, 0, s>>>(p);
-  else if (dtype == MUONH_DTYPE_BF16)
-    norm_columns_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  else
-    norm_columns_kernel<__half><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  void (*kernel)(NormParams) = dtype == MUONH_DTYPE_F32    ? norm_columns_kernel<float>
+                               : dtype == MUONH_DTYPE_BF16 ? norm_columns_kernel<__nv_bfloat16>
+                                                           : norm_columns_kernel<__half>;
+  return launch_programmatic(kernel, grid, 256, 0, s, p);
 }
 
 template <typename T>
 cudaError_t launch_wide(const NormParams& p, Pass pass, int grid, cudaStream_t s) {
-  if (pass == kForward)
-    norm_forward_wide_kernel<T><<<grid, kNormThreads, 0, s>>>(p);
-  else
-    norm_backward_wide_kernel<T><<<grid, kNormThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_programmatic(pass == kForward ? norm_forward_wide_kernel<T> : norm_backward_wide_kernel<T>, dim3(grid),
+                             kNormThreads, 0, s, p);
 }
 
 muonh_status check_rows(int64_t rows, int64_t n, int32_t dtype) {
@@ -1036,15 +1037,8 @@ extern "C" muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, 
     e = launch(p, dtype, sums ? kBackward : kBackwardRows, vec, elems, grid, smem, s);
   }
   if (e == cudaSuccess && sums && parts > 1) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1);
-    cfg.blockDim = dim3(32 * kJoinSlices);
-    cfg.stream = s;
-    cudaLaunchAttribute attr = programmatic_launch();
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, norm_join_kernel, static_cast<const float*>(p.part_w),
-                           static_cast<const float*>(p.part_b), dweight, dbias, parts, p.n);
+    e = launch_programmatic(norm_join_kernel, dim3((static_cast<unsigned>(n) + 31) / 32, dbias ? 2 : 1),
+                            32 * kJoinSlices, 0, s, p.part_w, p.part_b, dweight, dbias, parts, p.n);
   }
   if (e != cudaSuccess) return norm_fail(MUONH_ERR_CUDA, "launch of a layer norm backward kernel failed");
   return MUONH_OK;

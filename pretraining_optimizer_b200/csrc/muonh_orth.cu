@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 __global__ void __launch_bounds__(256)
     copy_stack_kernel(const uint16_t* from, int64_t from_stride, int64_t from_ld, uint16_t* to, int64_t to_stride,
                       int64_t to_ld, int64_t batch, int64_t rows, int cols, int lanes) {
+  wait_for_stream();
   const int per_block = 256 / lanes, lane = threadIdx.x % lanes;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes; r < batch * rows;
        r += static_cast<int64_t>(gridDim.x) * per_block) {
@@ -651,10 +652,9 @@ cudaError_t copy_stack(const void* from, int64_t from_stride, int64_t from_ld, v
   int lanes = 4;
   while (lanes < 32 && lanes < d.cols) lanes *= 2;
   const int64_t blocks = (d.batch * d.rows + 256 / lanes - 1) / (256 / lanes);
-  copy_stack_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sms)), 256, 0, s>>>(
-      static_cast<const uint16_t*>(from), from_stride, from_ld, static_cast<uint16_t*>(to), to_stride, to_ld, d.batch,
-      d.rows, static_cast<int>(d.cols), lanes);
-  return cudaGetLastError();
+  return launch_programmatic(copy_stack_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sms))), 256, 0,
+                             s, static_cast<const uint16_t*>(from), from_stride, from_ld, static_cast<uint16_t*>(to),
+                             to_stride, to_ld, d.batch, d.rows, static_cast<int>(d.cols), lanes);
 }
 
 muonh_status orth_fail(muonh_status st, const char* msg) {
