@@ -577,6 +577,9 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 // writes visible.  A kernel launched with the programmatic attribute (below) is
 // set up while they still run, and touches no global memory before this.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of that kind be set up from now on (once every block got
+// here) rather than when the blocks are done.
+__device__ __forceinline__ void let_next_set_up() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // --------------------------------------------------------- launch helpers
 inline cudaLaunchAttribute programmatic_launch() {

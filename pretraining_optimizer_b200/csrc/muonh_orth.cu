@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   __syncthreads();
   tc_fence_after();
   wait_for_stream();
+  if (p.late_below == 0) let_next_set_up();        // 1 us of the 21 to 45 of a small call; the norms lost by it
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_d = tmem + 256, tm_q = tmem + 384;   // r x r products; slice products use columns 0 .. 255
 
