@@ -372,8 +372,9 @@ muonh_status muonh_adamw_step(const muonh_adamw_tensor* tensors, int32_t n, cons
  *            hold whole 16-byte vectors move by vectors, others by elements.
  *   weight   n fp32 factors, or NULL for ones; bias n fp32, or NULL for none.
  *   mean, rstd   `rows` fp32 results, for the backward pass; rstd != NULL.
- * Sums are fp32.  A row that holds NaN or Inf gives NaN.  rows == 0 enqueues
- * nothing (the buffers may be NULL). */
+ * Sums are fp32, of squares too: values above 1.8e19 are beyond them.  A row
+ * that holds NaN or Inf gives NaN.  rows == 0 enqueues nothing (the buffers may
+ * be NULL). */
 muonh_status muonh_layer_norm(const void* x, int64_t ldx, void* y, int64_t ldy, const float* weight,
                               const float* bias, float* mean, float* rstd, int64_t rows, int64_t n, int32_t dtype,
                               float eps, void* stream);

@@ -9,7 +9,7 @@
 // four MMAs that use the same scale byte.  A 32-bit TMEM word per row holds the
 // bytes of four k-blocks (512 of k); the instruction descriptor picks the byte.
 //
-// Two shapes of the same kernel, persistent with one CTA per SM:
+// Three shapes of the same kernel, with one CTA per SM:
 //   pair    a cluster of two CTAs computes 256 x 256 tiles with cta_group::2, each
 //           CTA loading its 128 rows of A and half of the 256 rows of B.  A CTA
 //           then fetches 32 KB per 128 of k for 128 x 256 results, against 48 KB
@@ -20,9 +20,13 @@
 //           partial sums are added through distributed shared memory, in rank order.
 // Warps 0 and 3 load A and B by TMA (one k-block of 128 bytes is one 128-byte
 // swizzled row; a TMA instruction holds its thread for hundreds of cycles, so one
-// warp for both could not keep up), warp 2 gathers the scale words of both operands into shared memory, warp
-// 1 copies them to TMEM (tcgen05.cp) and issues the MMAs, and warps 4 to 11 take
-// the accumulator into registers, hand it back, round once and store.
+// warp for both could not keep up).  Warp 2 gathers the scale words of both
+// operands into shared memory; warp 1 copies them to TMEM (tcgen05.cp) and issues
+// the MMAs; warps 4 to 11 take the accumulator into registers, hand it back, round
+// once and store.
+//
+// 8192 x 6144 x 2048 to bf16: 98 us, 2.1 PFLOP/s at the power cap's 1.5 GHz; 256 x
+// 192 tiles with two accumulators took 108 (more operand traffic per product).
 //
 // The tensor cores' fp32 accumulation truncates, with an error that grows with
 // the number of products added up (5e-7 of the result's norm at k = 8192, for
