@@ -25,11 +25,12 @@
 // What bounds it, for one [128, 2048] bf16 matrix on each of 148 SMs (119k
 // cycles, 76 us): X X^T 28k cycles, reading 78 MB from HBM; the r x r iteration
 // 50k, a chain of 14 dependent products of 24 MMAs (128 x 128 x 16, 2k cycles
-// each with their hand-over) and as many passes of the epilogue (1.0 to 1.4k,
-// bound by its instructions: 512 threads, so 96 registers each); Q X 29k, 1.5k
-// per slice: its operands' reads, the slice's arrival and its result's way out
-// share the 128 bytes per cycle of shared memory.  The chain is what a single
-// matrix costs whatever its long side.
+// each with their hand-over, 1.5k without) and as many passes of the epilogue
+// (1.0 to 1.4k: TMEM reads, the split into pairs, two barriers; without its
+// stores it would be 5% of the chain shorter); Q X 29k, 1.5k per slice: its
+// operands' reads, the slice's arrival and its result's way out share the 128
+// bytes per cycle of shared memory.  The chain is what a single matrix costs
+// whatever its long side.
 //
 // Precision.  The products are 16-bit with fp32 accumulation.  X X^T is exact
 // up to the accumulation: X is used as it is.  The r x r operands are kept as
