@@ -329,8 +329,12 @@ __device__ __forceinline__ void write_parts(const NormParams& p, int G, float* j
     if (per_block == 1) continue;
     __syncthreads();
     for (int j = threadIdx.x; j < n; j += kNormThreads) {
+      // in fours: one chain over up to 64 groups rounds more often where the sums cancel
       float s = 0.f;
-      for (int g = 0; g < per_block; ++g) s += joined[static_cast<int64_t>(g) * n + j];
+      for (int g = 0; g < per_block; g += 4) {      // 4 groups at least
+        const float* c = joined + static_cast<int64_t>(g) * n + j;
+        s += (c[0] + c[n]) + (c[2 * n] + c[3 * n]);
+      }
       part[j] = s;
     }
   }
@@ -735,8 +739,8 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
   if (p.part_b) p.part_b[static_cast<int64_t>(blockIdx.y) * p.n + j] = sb;
 }
 
-// out[j] = sum over the partial rows, in their order within each of 16 slices
-// and then over the slices.  blockIdx.y: dw or db.
+// out[j] = sum over the partial rows: four sums within each of 16 slices, then a
+// tree.  blockIdx.y: dw or db.
 constexpr int kJoinSlices = 16;
 __global__ void __launch_bounds__(32 * kJoinSlices)
     norm_join_kernel(const float* part_w, const float* part_b, float* dw, float* db, int parts, int n) {
@@ -748,18 +752,24 @@ __global__ void __launch_bounds__(32 * kJoinSlices)
   if (!out) return;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float a = 0.f;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
   if (j < n) {
-#pragma unroll 4
-    for (int i = slice; i < parts; i += kJoinSlices) a += part[static_cast<int64_t>(i) * n + j];
+    for (int i = slice; i < parts; i += 4 * kJoinSlices)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * kJoinSlices < parts) a[k] += part[static_cast<int64_t>(i + k * kJoinSlices) * n + j];
   }
-  s[slice][lane] = a;
+  s[slice][lane] = (a[0] + a[1]) + (a[2] + a[3]);
   __syncthreads();
   if (slice == 0 && j < n) {
-    float sum = 0.f;
+    float sum[kJoinSlices];
 #pragma unroll
-    for (int i = 0; i < kJoinSlices; ++i) sum += s[i][lane];
-    out[j] = sum;
+    for (int i = 0; i < kJoinSlices; ++i) sum[i] = s[i][lane];
+#pragma unroll
+    for (int w = kJoinSlices / 2; w > 0; w /= 2)
+#pragma unroll
+      for (int i = 0; i < w; ++i) sum[i] += sum[i + w];
+    out[j] = sum[0];
   }
 }
 
