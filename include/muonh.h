@@ -408,14 +408,22 @@ muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void*
  *               out_stride in elements.  out may be x with the same strides;
  *               otherwise they must not overlap.
  *   ns_steps    0 .. 16;  eps >= 0 (a matrix of zeros gives zeros).
- * The result is off by the rounding to its type and, for an ill-conditioned X,
- * up to about 1e-3 of ||out|| (the r x r iterates are kept to 22 bits).
- * ||X||_F^2 is held in fp32, so norms must be below 1.8e19, and one below 1e-19
- * counts as zero; a matrix that holds NaN or Inf gives NaN throughout and leaves
+ * A direction that X lacks grows by |a| in each step of the factors' product Q,
+ * and Q's errors with it.  Where |a| >= 1, |Q| stays below 512 (five steps of the
+ * default coefficients: 485) and the iterates below 2, the r x r iterates are kept
+ * as fp16 pairs (22 bits; in the last product as a pair of the type), and the
+ * result is off by the rounding to its type and, for an X of nearly rank one, by
+ * up to 3e-3 of ||out|| in bf16 and 2e-3 in fp16 (some 1e-5 for X like noise).
+ * Otherwise the run is fp64 throughout (slower; the iterates too are kept in fp64),
+ * and off by the rounding to the type and about |a|^ns_steps 1e-16.
+ * In pairs ||X||_F^2 is held in fp32, so norms must be below 1.8e19, and one below
+ * 1e-19 counts as zero; a matrix that holds NaN or Inf gives NaN throughout and leaves
  * the others alone.
  *   workspace   16-byte aligned device scratch of muonh_orthogonalize_workspace
- *               bytes: 0 where base pointers and strides are multiples of 16
- *               bytes, else room for a copy of the stacks that are not.
+ *               bytes.  In pairs: 0 where base pointers and strides are multiples
+ *               of 16 bytes, else room for a copy of the stacks that are not.  In
+ *               fp64: 256 MB at most, or what one matrix needs (8 bytes for each of
+ *               its elements, and up to 21 r x r matrices).
  * UNSUPPORTED where the smaller side is above 128. */
 typedef struct {
   const void* x;

@@ -158,7 +158,7 @@ void scale_exponents(float a, float b, float c, int steps, int prec, int32_t* ex
 // [0, smax], smax the bound on every iterate's singular values (at s = 0 it
 // is a^run).  The products A_k p(A_k) are bounded like A (they act as
 // s_k s_{k+1}) and share A's scale.
-int q_exponent(float a, float b, float c, int run, double smax) {
+double q_bound(float a, float b, float c, int run, double smax) {
   double qmax = 0.0;
   const int n = 8192;
   for (int i = 0; i <= n; ++i) {
@@ -168,9 +168,12 @@ int q_exponent(float a, float b, float c, int run, double smax) {
       q *= f;
       s *= f;
     }
-    qmax = std::max(qmax, std::fabs(q));
+    if (!(std::fabs(q) <= qmax)) qmax = std::fabs(q);   // NaN (an overflow) stays
   }
-  return safe_exponent(std::max(qmax * 1.02, 1e-30));
+  return qmax;
+}
+int q_exponent(float a, float b, float c, int run, double smax) {
+  return safe_exponent(std::max(q_bound(a, b, c, run, smax) * 1.02, 1e-30));
 }
 
 // Bound on the singular values of every iterate (the s_all of scale_exponents).
@@ -196,25 +199,41 @@ int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 void muonh::set_error_message(const char* msg) { g_last_error = msg; }
 
-void muonh::ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq) {
-  // the bounds sample the scalar maps at thousands of points; a program uses
-  // one set of coefficients over and over
-  struct Memo {
-    float a, b, c;
-    int steps = -1;
-    int32_t ea, eb, eq[kMaxChainSteps];
-  };
-  static thread_local Memo memo;
+namespace {
+
+// The bounds sample the scalar maps at thousands of points; a program uses one
+// set of coefficients over and over.
+struct ChainMemo {
+  float a, b, c;
+  int steps = -1;
+  int32_t ea, eb, eq[kMaxChainSteps];
+  int run;
+};
+
+const ChainMemo& chain_memo(float a, float b, float c, int steps) {
+  static thread_local ChainMemo memo;
   if (memo.steps != steps || memo.a != a || memo.b != b || memo.c != c) {
     int32_t ex, ec;
     scale_exponents(a, b, c, steps, P_FP16, &ex, &memo.ea, &ec, &memo.eb);
     const double smax = iterate_bound(a, b, c, steps);
     for (int k = 0; k < steps; ++k) memo.eq[k] = q_exponent(a, b, c, k + 1, smax);
+    memo.run = 0;
+    if (std::fabs(a) >= 1.f && smax <= kPairIterates)
+      while (memo.run < steps && q_bound(a, b, c, memo.run + 1, smax) <= kPairGrowth) ++memo.run;
     memo.a = a;
     memo.b = b;
     memo.c = c;
     memo.steps = steps;
   }
+  return memo;
+}
+
+}  // namespace
+
+int muonh::ns_chain_run(float a, float b, float c, int steps) { return chain_memo(a, b, c, steps).run; }
+
+void muonh::ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq) {
+  const ChainMemo& memo = chain_memo(a, b, c, steps);
   *ea = memo.ea;
   *eb = memo.eb;
   std::copy(memo.eq, memo.eq + steps, eq);

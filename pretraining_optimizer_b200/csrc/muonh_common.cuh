@@ -463,6 +463,23 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int ab_bf16, int 
 constexpr int kMaxChainSteps = 16;
 void ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t* eb, int32_t* eq);
 
+// How many of these factors fp16 pairs hold in one run (0: not even one).  A
+// direction that X lacks grows by |a| in each step of the product while the
+// others stay near one, and the pairs' errors, relative to the largest, with it.
+// By emulation of the kernel's arithmetic on nearly and exactly low-rank
+// matrices the result was off by up to 2.7e-3 of its norm (fp16: 1.6e-3) at a
+// growth of 485 (five steps of the default coefficients), by 1e-2 at 1670, by 0.1 at
+// 2e4, and overflowed at 2e5.  Factors below one (|a| < 1) would leave the pairs'
+// range at the other end.
+constexpr double kPairGrowth = 512.0;    // bound on the product of the factors
+constexpr double kPairIterates = 2.0;    // ... and on the iterates' singular values (1.2 by default)
+int ns_chain_run(float a, float b, float c, int steps);
+
+// The same run in fp64, for desc whose coefficients pairs do not hold: scratch
+// bytes (16-byte aligned), and the launches.  desc has been checked.
+size_t orthogonalize_fp64_workspace(const muonh_orthogonalize_desc& d);
+cudaError_t orthogonalize_fp64(const muonh_orthogonalize_desc& d, void* workspace, cudaStream_t s);
+
 // 3-D map over a stack of 16-bit matrices (`batch` of rows x cols, row stride
 // ld and matrix stride `stride` in elements) with 64-column boxes of
 // box_rows rows (128-byte swizzle).

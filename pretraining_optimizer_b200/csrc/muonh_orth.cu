@@ -38,6 +38,8 @@
 // with single fp16 operands the Gram-space form loses the small singular
 // directions (errors of 0.1 and more on ill-conditioned updates, by emulation,
 // against 2e-4 with pairs).  Q enters the last product as a pair of X's type.
+// Pairs hold five steps of the default coefficients; where ns_chain_run finds that
+// they do not hold all of a run, it is muonh_orth_fp64.cu's.
 // The tensor cores' accumulation truncates, so at most kGramChunk slices are
 // accumulated in TMEM before they are added in IEEE fp32 registers.
 // The result is rounded once to X's type.
@@ -739,6 +741,11 @@ int pick_cluster(bool bf16, int64_t batch, int slices, int dev) {
   return ranks;
 }
 
+// Whether the r x r iterates can be kept as pairs; else the run is muonh_orth_fp64.cu's.
+bool pairs_hold(const muonh_orthogonalize_desc& d) {
+  return ns_chain_run(d.ns_a, d.ns_b, d.ns_c, d.ns_steps) >= d.ns_steps;
+}
+
 size_t copy_bytes(const muonh_orthogonalize_desc& d) {
   return static_cast<size_t>(d.batch) * d.rows * up8(d.cols) * 2;
 }
@@ -750,6 +757,8 @@ using namespace muonh;
 
 extern "C" size_t muonh_orthogonalize_workspace(const muonh_orthogonalize_desc* d) {
   if (!d || d->batch < 1 || d->rows < 1 || d->cols < 1) return 0;
+  if (std::min(d->rows, d->cols) > kSide || d->ns_steps < 0 || d->ns_steps > kMaxSteps) return 0;   // refused
+  if (!pairs_hold(*d)) return orthogonalize_fp64_workspace(*d);
   size_t n = 0;
   if (!tma_stack(d->x, d->x_stride, d->ldx, d->batch, d->rows)) n += copy_bytes(*d);
   if (!tma_stack(d->out, d->out_stride, d->ldo, d->batch, d->rows)) n += copy_bytes(*d);
@@ -761,11 +770,16 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
   set_error_message("");
   if (const muonh_status st = check_orth(d)) return st;
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return MUONH_OK;
-  if (workspace_bytes < muonh_orthogonalize_workspace(d) || (muonh_orthogonalize_workspace(d) && !workspace))
+  const size_t scratch = muonh_orthogonalize_workspace(d);
+  if (workspace_bytes < scratch || (scratch && !workspace))
     return orth_fail(MUONH_ERR_INVALID_ARG, "the workspace is smaller than muonh_orthogonalize_workspace says");
   if (reinterpret_cast<uintptr_t>(workspace) & 15)
     return orth_fail(MUONH_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!pairs_hold(*d))
+    return orthogonalize_fp64(*d, workspace, s) == cudaSuccess
+               ? MUONH_OK
+               : orth_fail(MUONH_ERR_CUDA, "launch of a kernel of the fp64 orthogonalize run failed");
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

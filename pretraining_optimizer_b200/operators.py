@@ -171,7 +171,9 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     [batch, rows, cols], bf16 or fp16, unit column stride, any other strides),
     for matrices whose smaller side is at most 128: one Muon update per
     attention head.  Returns a tensor of x's shape and type, laid out like x
-    where x has no gaps, or `out`, which may be x."""
+    where x has no gaps, or `out`, which may be x.  Runs whose factors grow
+    beyond 512 (more than five of the default steps) are computed in fp64, and
+    take longer."""
     _types()
     _tensor(x, "x", (torch.bfloat16, torch.float16))
     handle = _here(x, stream)
