@@ -85,6 +85,18 @@ def test_steps_on_matrices_of_low_rank(steps, kind, dtype):
     operator_status()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind", ["plain", "spiked", "rank"])
+@pytest.mark.parametrize("shape", [(3, 128, 512), (2, 64, 64), (2, 128, 128), (2, 700, 128), (3, 48, 300), (1, 128, 8192)])
+def test_five_steps_are_within_the_documented_bound(shape, kind, dtype):
+    """Ill-conditioned updates, for which bounds from the spectrum alone are several times the result's norm."""
+    t = _t()
+    from pretraining_optimizer_b200 import orthogonalize
+    from test_gpu_orthogonalize import _spectrum
+    x = t.from_numpy(_spectrum(np.random.default_rng(4), *shape, kind)).to("cuda:0", _dtype(dtype))
+    check(x, orthogonalize(x), 5)
+
+
 @pytest.mark.parametrize("coeffs,steps", [(CUBIC, 15), (CUBIC, 16), ((2.0, -1.5, 0.5), 9), ((2.0, -1.5, 0.5), 10),
                                           ((20.0, -40.0, 21.0), 3), ((0.5, 0.25, 0.0), 6), ((0.0, 1.0, 0.0), 2),
                                           ((0.0, 0.0, 1.0), 1), ((-3.0, 3.0, -1.0), 4)])
