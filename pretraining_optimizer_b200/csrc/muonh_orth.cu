@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     epilogue_sync();
     d = (trace[0] + trace[1]) + (trace[2] + trace[3]);
     const float norm = sqrtf(d) + p.eps;
-    scale = norm > 0.f ? 1.f / norm : (norm == 0.f ? 0.f : norm);   // zeros stay zeros, NaN stays NaN
+    // zeros stay zeros; a norm that is not finite makes the matrix NaN (1 / Inf would leave finite elements at 0)
+    scale = norm > 0.f ? (isinf(norm) ? __int_as_float(0x7fffffff) : 1.f / norm) : (norm == 0.f ? 0.f : norm);
     // from here on acc is 2^ea A_k
     const float start = scale * exp2i(p.ea);
 #pragma unroll
