@@ -373,8 +373,9 @@ muonh_status muonh_adamw_step(const muonh_adamw_tensor* tensors, int32_t n, cons
  *   weight   n fp32 factors, or NULL for ones; bias n fp32, or NULL for none.
  *   mean, rstd   `rows` fp32 results, for the backward pass; rstd != NULL.
  * Sums are fp32, of squares too: values above 1.8e19 are beyond them.  A row
- * that holds NaN or Inf gives NaN.  rows == 0 enqueues nothing (the buffers may
- * be NULL). */
+ * that holds NaN gives NaN, and so does one that holds Inf in the layer norm.  In
+ * the RMS norm Inf makes rstd 0: infinite elements give NaN, finite ones the bias.
+ * Other rows are left alone.  rows == 0 enqueues nothing (the buffers may be NULL). */
 muonh_status muonh_layer_norm(const void* x, int64_t ldx, void* y, int64_t ldy, const float* weight,
                               const float* bias, float* mean, float* rstd, int64_t rows, int64_t n, int32_t dtype,
                               float eps, void* stream);

@@ -28,3 +28,25 @@ def test_a_matrix_with_infinity_is_nan_throughout_at_every_step_count(steps, dty
         if dtype == "bf16":
             huge = orthogonalize(x[:1] * 2.0 ** 66, ns_steps=steps)
             assert bool(huge.isnan().all()) if steps <= 5 else bool(huge.isfinite().all())
+
+
+@pytest.mark.parametrize("n", [100, 300, 2048, 9000])
+@pytest.mark.parametrize("rms", [False, True])
+def test_rows_with_nan_or_infinity(rms, n):
+    """NaN: the row is NaN.  Inf: NaN for the layer norm; for the RMS norm rstd is 0, so the infinite elements are NaN
+    and the finite ones the bias."""
+    import torch
+    from pretraining_optimizer_b200 import layer_norm
+    x, w, b = _randn(2, 9, n), _randn(3, n), _randn(4, n)
+    clean, _, clean_rstd = layer_norm(x, w, b, rms=rms)
+    x[2, 5], x[6, n - 1], x[7, 0] = float("nan"), float("inf"), float("-inf")
+    y, _, rstd = layer_norm(x, w, b, rms=rms)
+    assert bool(y[2].isnan().all()) and bool(rstd[2].isnan())
+    for row, at in ((6, n - 1), (7, 0)):
+        if rms:
+            finite = torch.arange(n, device="cuda") != at
+            assert float(rstd[row]) == 0 and bool(y[row, at].isnan()) and torch.equal(y[row, finite], b[finite])
+        else:
+            assert bool(y[row].isnan().all()) and bool(rstd[row].isnan())
+    keep = [0, 1, 3, 4, 5, 8]
+    assert torch.equal(y[keep], clean[keep]) and torch.equal(rstd[keep], clean_rstd[keep])
