@@ -430,11 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // no MMA may still write TMEM when the CTA frees it
-      if (leader) umma_commit(drain);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
-      }
+      if (leader) commit(drain);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -566,6 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {
+    // no MMA may still write TMEM when a CTA frees it (the last commit arrives in both CTAs of a pair)
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+    }
+  }
   if (PAIR) cluster_sync();                      // neither CTA's memory is in use by the other
   tc_fence_after();
   if (warp == 1) {

@@ -755,10 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PREC, MODE>:
         umma_commit_pair(&tfull[acc]);
         td = next;
       }
-      umma_commit(drain);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
-      }
+      umma_commit_pair(drain);
     }
     __syncwarp();
   } else {
@@ -1102,6 +1099,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<PREC, MODE>:
 
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {             // the leader's last commit arrives in both CTAs
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+    }
+  }
   cluster_sync();              // the leader's MMAs into both CTAs' TMEM have drained
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
