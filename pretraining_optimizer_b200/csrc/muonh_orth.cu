@@ -66,10 +66,14 @@ constexpr int kOrthThreads = 64 + kEpiThreads;    // warp 0 TMA, warp 1 MMA
 constexpr int kGramChunk = 16;                    // slices (2048 columns) per TMEM accumulation
 constexpr int kMaxSteps = kMaxChainSteps;
 // With several matrices per SM all SMs read X, iterate and write at the same
-// time, and HBM idles during the r x r iterations.  Half of the SMs start a
-// quarter of a matrix later: 896 x [128, 2048] took 437 us without, 399 with 15
-// us, 406 with 25 us; below four matrices per SM the delay costs what it gives.
-constexpr int kLateNs = 15000;
+// time, and HBM idles during the r x r iterations.  Half of the SMs start later by
+// about what one walk over X takes.  Against none, at 600 to 1500 matrices of 16,
+// 64 and 128 rows and 0 to 5 steps: 2 to 9% faster with 64 and 128 rows of 1024 and
+// more, even with 16; shorter ones read too little to be apart.  (15 us whatever the
+// length, as for 2048, cost up to 17% where a matrix takes less than that.)
+constexpr int kLateSliceNs = 940;                 // of a walk: 28k cycles for 16 slices
+constexpr int kLateMostNs = 30000;
+constexpr int kLateSlices = 4;
 constexpr int kLateWaves = 4;
 constexpr int kMaxCluster = 8;
 
@@ -84,7 +88,8 @@ struct OrthParams {
   // step k; and the final Q
   int32_t ea, eb, eq[kMaxSteps], eq_last;
   int32_t rows, cols;        // of X, for skipping stores outside
-  int32_t late_below;        // odd CTAs below this number start kLateNs late
+  int32_t late_below;        // odd CTAs below this number start late_ns late
+  int32_t late_ns;
   int32_t used;              // small side rounded up to 64 or 128: columns and k of the r x r products
 };
 
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 
   if (static_cast<int>(blockIdx.x) < p.late_below && (blockIdx.x & 1)) {
     const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < kLateNs) __nanosleep(500);
+    while (globaltimer() - t0 < static_cast<uint64_t>(p.late_ns)) __nanosleep(500);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
@@ -819,7 +824,8 @@ extern "C" muonh_status muonh_orthogonalize(const muonh_orthogonalize_desc* d, v
                        : allow_shared(orthogonalize_kernel<false>, done[0], kOrthSmem);
   if (e != cudaSuccess) return orth_fail(MUONH_ERR_CUDA, "the kernel's shared memory was refused");
   const int ranks = pick_cluster(bf16, d->batch, p.slices, dev);
-  p.late_below = d->batch >= static_cast<int64_t>(kLateWaves) * sms ? sms : 0;
+  p.late_below = d->batch >= static_cast<int64_t>(kLateWaves) * sms && p.slices >= kLateSlices ? sms : 0;
+  p.late_ns = static_cast<int32_t>(std::min<int64_t>(int64_t(kLateSliceNs) * p.slices, kLateMostNs));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(d->batch * ranks));
   cfg.blockDim = dim3(kOrthThreads);

@@ -50,3 +50,18 @@ def test_rows_with_nan_or_infinity(rms, n):
             assert bool(y[row].isnan().all()) and bool(rstd[row].isnan())
     keep = [0, 1, 3, 4, 5, 8]
     assert torch.equal(y[keep], clean[keep]) and torch.equal(rstd[keep], clean_rstd[keep])
+
+
+@pytest.mark.parametrize("shape", [(600, 64, 520), (610, 700, 33), (592, 128, 513), (591, 16, 1024), (600, 5, 4100)])
+def test_stacks_whose_ctas_start_late(shape):
+    """Four matrices per SM and more (and one fewer), with long sides on both sides of the late start's limit."""
+    import torch
+    from pretraining_optimizer_b200 import operator_status, orthogonalize
+    from test_gpu_orthogonalize import check
+    x = (1e-3 * _randn(11, *shape)).bfloat16()
+    for steps in (0, 5):
+        got = orthogonalize(x, ns_steps=steps)
+        assert torch.equal(got, orthogonalize(x, ns_steps=steps))
+        some = [0, 1, 147, 148, 149, shape[0] - 1]
+        check(x[some], got[some], steps)
+    operator_status()
