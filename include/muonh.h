@@ -486,7 +486,10 @@ muonh_status muonh_block_matmul(const muonh_block_operand* a, const muonh_block_
 
 /* MUONH_ERR_TIMEOUT if a device wait gave up in an operator call above since
  * the previous call (then clears the record), else OK; synchronises `stream`,
- * which must be the one, or ordered after the ones, that the calls ran on. */
+ * which must be the one, or ordered after the ones, that the calls ran on, and
+ * belong to the current device.  The record is one per device, for the calls of
+ * all threads and streams: the first to ask gets it, whoever's call gave up, so a
+ * program with several threads asks in one place and stops them all. */
 muonh_status muonh_operator_status(void* stream);
 
 /* Diagnostic of the failure path every pipelined kernel uses (the report has

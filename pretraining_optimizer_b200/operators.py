@@ -302,9 +302,12 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
 
 
 def operator_status(stream=None) -> None:
-    """Synchronises `stream` (default: the current one) and raises MuonHError
-    if a device wait gave up in an operator call since the previous check."""
+    """Synchronises `stream` (default: the current one) and raises MuonHError if
+    a device wait gave up in an operator call on its device since the previous
+    check.  There is one record per device, which reading clears: it holds for
+    the calls of all threads and streams, and the first to ask gets it."""
+    _types()
     if stream is None:
-        _types()
         stream = torch.cuda.current_stream()
-    _check(library().muonh_operator_status(stream.cuda_stream))
+    with torch.cuda.device(stream.device):
+        _check(library().muonh_operator_status(stream.cuda_stream))
