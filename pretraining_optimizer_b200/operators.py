@@ -188,7 +188,8 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     rows, cols = shape[-2], shape[-1]
     lib = library()
     if out is None:
-        out = torch.empty_like(x)
+        # matrices that overlap along a row have no layout of their own to keep
+        out = torch.empty_like(x) if batch < 2 or xs >= cols else torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         _tensor(out, "out", (x.dtype,), x.device)
         if out.shape != shape:

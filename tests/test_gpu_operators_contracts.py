@@ -52,6 +52,23 @@ def test_rows_with_nan_or_infinity(rms, n):
     assert torch.equal(y[keep], clean[keep]) and torch.equal(rstd[keep], clean_rstd[keep])
 
 
+def test_matrices_that_overlap_in_the_input():
+    """A window that slides over one buffer: any batch stride is allowed on the way in."""
+    import torch
+    from pretraining_optimizer_b200 import orthogonalize
+    buffer = _randn(5, 4000).bfloat16()
+    for shape, stride in (((4, 1, 8), (1, 8, 1)), ((4, 3, 8), (1, 8, 1)), ((5, 16, 40), (3, 40, 1)), ((3, 4, 8), (0, 8, 1)),
+                          ((6, 16, 40), (40, 40, 1))):
+        x = buffer.as_strided(shape, stride)
+        got = orthogonalize(x)
+        assert got.shape == x.shape and torch.equal(got, orthogonalize(x.contiguous()))
+        # the result's matrices are apart: clearing one leaves the others
+        want = got.clone()
+        want[0] = 0
+        got[0] = 0
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("shape", [(600, 64, 520), (610, 700, 33), (592, 128, 513), (591, 16, 1024), (600, 5, 4100)])
 def test_stacks_whose_ctas_start_late(shape):
     """Four matrices per SM and more (and one fewer), with long sides on both sides of the late start's limit."""
