@@ -166,6 +166,20 @@ def _stack(t, what: str):
     return t.data_ptr(), strides[0] if len(shape) == 3 else 0, max(strides[-2], cols)
 
 
+def _apart(batch, rows, cols, stride, ld):
+    """Whether no element of a stack with these strides (ld >= cols) belongs to two of its matrices."""
+    height = (rows - 1) * ld + cols
+    if batch < 2 or stride >= height:                                  # one behind the other
+        return True
+    if stride < cols or ld >= (batch - 1) * stride + cols:             # side by side in their rows
+        return stride >= cols
+    for shift in range(stride, min((batch - 1) * stride, height) + 1, stride):   # rows of one between another's
+        row, col = divmod(shift, ld)
+        if (row < rows and col < cols) or (row + 1 < rows and ld - col < cols):
+            return False
+    return True
+
+
 def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, stream=None):
     """The Newton-Schulz output of each matrix of a stack x ([rows, cols] or
     [batch, rows, cols], bf16 or fp16, unit column stride, any other strides),
@@ -195,7 +209,7 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
         if out.shape != shape:
             raise ValueError("out must have x's shape")
     op, os_, ldo = _stack(out, "out")
-    if batch > 1 and os_ < cols:
+    if not _apart(batch, rows, cols, os_, ldo):
         raise ValueError("out must have matrices that do not overlap")
     d = OrthogonalizeDesc(xp, op, batch, rows, cols, xs, ldx, os_, ldo, _types()[x.dtype], int(ns_steps), a, b, c, eps)
     size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))

@@ -69,6 +69,24 @@ def test_matrices_that_overlap_in_the_input():
         assert torch.equal(got, want)
 
 
+def test_results_whose_matrices_overlap_are_refused():
+    import torch
+    from pretraining_optimizer_b200 import orthogonalize
+    buffer = torch.zeros(20000, device="cuda", dtype=torch.bfloat16)
+    for shape, stride in (((3, 4, 8), (8, 8, 1)), ((3, 4, 8), (24, 8, 1)), ((3, 4, 8), (12, 16, 1)), ((9, 4, 8), (8, 64, 1)),
+                          ((2, 3, 5), (20, 10, 1)), ((2, 4, 8), (4, 8, 1)), ((2, 4, 8), (0, 8, 1))):
+        x = _randn(6, *shape).bfloat16()
+        with pytest.raises(ValueError, match="overlap"):
+            orthogonalize(x, out=buffer.as_strided(shape, stride))
+    assert not bool(buffer.any())
+    # one behind the other, side by side, and row by row in turn
+    for shape, stride in (((3, 4, 8), (32, 8, 1)), ((3, 4, 8), (40, 8, 1)), ((8, 4, 8), (8, 64, 1)), ((2, 3, 5), (15, 10, 1)),
+                          ((2, 3, 5), (5, 10, 1)), ((3, 1, 8), (8, 8, 1)), ((1, 4, 8), (0, 8, 1))):
+        x = _randn(7, *shape).bfloat16()
+        out = buffer.as_strided(shape, stride)
+        assert torch.equal(orthogonalize(x, out=out), orthogonalize(x))
+
+
 @pytest.mark.parametrize("shape", [(600, 64, 520), (610, 700, 33), (592, 128, 513), (591, 16, 1024), (600, 5, 4100)])
 def test_stacks_whose_ctas_start_late(shape):
     """Four matrices per SM and more (and one fewer), with long sides on both sides of the late start's limit."""

@@ -28,3 +28,15 @@ def test_operator_status_reads_the_streams_device(monkeypatch):
     operators.operator_status(types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=42))
     operators.operator_status()
     assert seen == [(42, 1), (7, 0)] and current == [0]
+
+
+def test_which_stacks_are_apart():
+    """Against the addresses themselves, for every small stack with unit column stride."""
+    for batch in (1, 2, 3, 5):
+        for rows in (1, 2, 4):
+            for cols in (1, 3, 4):
+                for ld in range(cols, 4 * cols + 2):
+                    for stride in range(0, 40):
+                        at = [b * stride + i * ld + j for b in range(batch) for i in range(rows) for j in range(cols)]
+                        got = operators._apart(batch, rows, cols, stride, ld)
+                        assert got == (len(set(at)) == len(at)), (batch, rows, cols, stride, ld)
