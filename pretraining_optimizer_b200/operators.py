@@ -6,6 +6,10 @@ is in the library's CUDA kernels.  Each call runs on the device of its tensors,
 on `stream` or that device's current stream.  A given stream is also the one
 that results and scratch are allocated on, as under `torch.cuda.stream(stream)`.
 
+No call records an autograd graph: results of tensors that require gradients do
+not, and the backward calls are the program's own.  A write to `out` counts as an
+in-place change, so a graph that saved the tensor refuses its backward pass.
+
 The smallest calls are bound by the host, so the usual case (the current stream
 of the current device) takes no context manager and no Stream object.
 """
@@ -81,6 +85,13 @@ def _like(x):
     return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _written(out):
+    """`out`, whose change autograd is told of."""
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+    return out
+
+
 def _vector(t, what: str, n: int, device):
     if t is None:
         return None
@@ -95,7 +106,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     norm with rms=True: y = (x - mean) rstd weight + bias.  weight and bias are
     fp32, as adamw_step keeps them.  Returns (y, mean, rstd): y in x's type (or
     `out`, which may be x), mean (None for the RMS norm) and rstd fp32, one per
-    row, for layer_norm_backward."""
+    row, for layer_norm_backward (no autograd graph is recorded).  The leading
+    dimensions of x, and of `out`, have to be rows one stride apart: all heads
+    inside a wider projection are two strides and take a .contiguous()."""
     _tensor(x, "x", _types())
     handle = _here(x, stream)
     if handle is None:
@@ -106,7 +119,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     xp, rows, n, ldx = _rows(x, "x")
     wp = _vector(weight, "weight", n, device)
     bp = _vector(bias, "bias", n, device)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _like(x)
         op, ldo = out.data_ptr(), n
     else:
@@ -119,14 +133,15 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     rstd = torch.empty(*lead, dtype=torch.float32, device=device)
     _check(library().muonh_layer_norm(xp, ldx, op, ldo, wp, bp, None if rms else mean.data_ptr(), rstd.data_ptr(),
                                       rows, n, _types()[dtype], eps, handle))
-    return out, mean, rstd
+    return _written(out) if given else out, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, bias=False, stream=None):
     """Gradients of layer_norm at x for the gradient dy of its result (x's shape
-    and type): (dx, dweight, dbias).  mean and rstd are what layer_norm gave;
-    mean None means the RMS norm.  dweight (None where weight is None) and dbias
-    (None unless bias is true) are fp32, as adamw_step reads them."""
+    and type, rows one stride apart): (dx, dweight, dbias).  mean and rstd are
+    what layer_norm gave; mean None means the RMS norm.  dweight (None where
+    weight is None) and dbias (None unless bias is true) are fp32, as adamw_step
+    reads them, of these rows alone: microbatches' are added by the program."""
     _tensor(x, "x", _types())
     handle = _here(x, stream)
     if handle is None:
@@ -184,7 +199,7 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     """The Newton-Schulz output of each matrix of a stack x ([rows, cols] or
     [batch, rows, cols], bf16 or fp16, unit column stride, any other strides),
     for matrices whose smaller side is at most 128: one Muon update per
-    attention head.  Returns a tensor of x's shape and type, laid out like x
+    attention head (an fp32 momentum is cast first).  Returns a tensor of x's shape and type, laid out like x
     where x has no gaps, or `out`, which may be x.  Runs whose factors grow
     beyond 512 (more than five of the default steps) are computed in fp64, and
     take longer."""
@@ -201,7 +216,8 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     batch = shape[0] if len(shape) == 3 else 1
     rows, cols = shape[-2], shape[-1]
     lib = library()
-    if out is None:
+    given = out is not None
+    if not given:
         # matrices that overlap along a row have no layout of their own to keep
         out = torch.empty_like(x) if batch < 2 or xs >= cols else torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
@@ -215,7 +231,7 @@ def orthogonalize(x, *, ns_steps=5, ns_coeffs=QUINTIC, eps=1e-7, out=None, strea
     size = lib.muonh_orthogonalize_workspace(ctypes.byref(d))
     work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     _check(lib.muonh_orthogonalize(ctypes.byref(d), None if work is None else work.data_ptr(), size, handle))
-    return out
+    return _written(out) if given else out
 
 
 def _matrix(t, what: str):
@@ -298,7 +314,8 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
     bo, n, kb = _block_operand(b, b_scale, "b", a.device)
     if k != kb:
         raise ValueError("a and b must have the same number of columns")
-    if out is None:
+    given = out is not None
+    if not given:
         if accumulate:
             raise ValueError("accumulate needs out")
         dtype = torch.bfloat16 if dtype is None else dtype
@@ -313,7 +330,7 @@ def block_matmul(a, a_scale, b, b_scale, *, dtype=None, out=None, accumulate=Fal
         op, _, _, ldo = _matrix(out, "out")
     _check(library().muonh_block_matmul(ctypes.byref(ao), ctypes.byref(bo), k, op, ldo, _types()[out.dtype],
                                         1 if accumulate else 0, handle))
-    return out
+    return _written(out) if given else out
 
 
 def operator_status(stream=None) -> None:

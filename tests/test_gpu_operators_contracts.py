@@ -87,6 +87,25 @@ def test_results_whose_matrices_overlap_are_refused():
         assert torch.equal(orthogonalize(x, out=out), orthogonalize(x))
 
 
+def test_writes_to_out_are_seen_by_autograd():
+    """A tensor that a graph saved and an operator then overwrites may not go into its gradient unnoticed."""
+    import torch
+    import pretraining_optimizer_b200 as P
+    q, s = P.block_quantize(_randn(8, 32, 128))
+    calls = (lambda t: P.layer_norm(t, out=t), lambda t: P.block_matmul(q, s, q, s, out=t),
+             lambda t: P.orthogonalize(t.bfloat16(), out=t))
+    for call, dtype in zip(calls, (torch.float32, torch.float32, torch.bfloat16)):
+        saved = _randn(9, 32, 32).to(dtype)
+        w = torch.ones(32, 32, device="cuda", dtype=dtype, requires_grad=True)
+        loss = (w * saved).sum()
+        call(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        t = _randn(10, 32, 32)
+        P.layer_norm(t, out=t)
+
+
 @pytest.mark.parametrize("shape", [(600, 64, 520), (610, 700, 33), (592, 128, 513), (591, 16, 1024), (600, 5, 4100)])
 def test_stacks_whose_ctas_start_late(shape):
     """Four matrices per SM and more (and one fewer), with long sides on both sides of the late start's limit."""
