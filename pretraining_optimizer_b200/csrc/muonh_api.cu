@@ -168,7 +168,7 @@ double q_bound(float a, float b, float c, int run, double smax) {
       q *= f;
       s *= f;
     }
-    if (!(std::fabs(q) <= qmax)) qmax = std::fabs(q);   // NaN (an overflow) stays
+    qmax = std::max(qmax, std::fabs(q));
   }
   return qmax;
 }

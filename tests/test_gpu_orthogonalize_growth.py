@@ -164,6 +164,21 @@ def test_long_runs_of_zero_tiny_and_non_finite_matrices():
     assert bool((orthogonalize(x[:1], ns_steps=8, eps=0.0) == 0).all())
 
 
+@pytest.mark.parametrize("cols", [264, 203])
+def test_long_runs_of_matrices_far_apart(cols):
+    """Matrices more than 2^31 elements apart: the bits of the compact stack, in place too."""
+    t = _t()
+    from pretraining_optimizer_b200 import orthogonalize
+    x = t.from_numpy(matrices("4+1e-2", 3, 32, cols)).to("cuda:0", t.bfloat16)
+    want = orthogonalize(x, ns_steps=8)
+    far = 2 ** 31 + 64
+    view = t.empty(2 * far + 32 * cols, dtype=t.bfloat16, device="cuda:0").as_strided(x.shape, (far, cols, 1))
+    view.copy_(x)
+    assert t.equal(orthogonalize(view, ns_steps=8).contiguous(), want)
+    orthogonalize(view, ns_steps=8, out=view)
+    assert t.equal(view.contiguous(), want)
+
+
 def test_long_runs_on_a_side_stream_and_in_a_graph():
     t = _t()
     from pretraining_optimizer_b200 import orthogonalize

@@ -35,6 +35,8 @@ def test_scratch_is_bounded():
     assert _scratch(6, batch=1, rows=128, cols=2048) >= matrix
     assert _scratch(6, batch=896, rows=128, cols=2048) <= 2 ** 28
     assert _scratch(6, batch=2 ** 24, rows=1, cols=1) <= 2 ** 28
+    # sizes that the call refuses, and whose products do not fit in 64 bits
+    assert _scratch(6, batch=2 ** 62) == _scratch(6, rows=4, cols=2 ** 62) == _scratch(6, rows=2 ** 62, cols=4) == 0
     # one matrix at least, however long
     assert 2 ** 30 * 8 <= _scratch(6, batch=3, rows=1, cols=2 ** 30) <= 2 ** 30 * 8 + 2 ** 20
 
