@@ -25,8 +25,9 @@
 // the MMAs; warps 4 to 11 take the accumulator into registers, hand it back, round
 // once and store.
 //
-// 8192 x 6144 x 2048 to bf16: 98 us, 2.1 PFLOP/s at the power cap's 1.5 GHz; 256 x
-// 192 tiles with two accumulators took 108 (more operand traffic per product).
+// 8192 x 6144 x 2048 to bf16: 94 us in a burst, 111 us (1.85 PFLOP/s) under the power
+// cap at some 1.7 GHz; 256 x 192 tiles with two accumulators took 108 against 98 side
+// by side (more operand traffic per product).
 //
 // The tensor cores' fp32 accumulation truncates, with an error that grows with
 // the number of products added up (5e-7 of the result's norm at k = 8192, for

@@ -10,7 +10,8 @@
 // backward pass reads dy and x and writes dx once.  A group of G threads holds
 // one row in registers, so a row is read once whatever the number of reductions
 // over it, and its next rows are on their way meanwhile:
-//   up to 32 lanes per row (n <= 512)     the next row is loaded into registers
+//   up to 32 lanes per row (n <= 256; backward, 16-bit rows in packs: 512)
+//            the next row is loaded into registers
 //   128 or 512 threads per row (n <= 8192) the next rows are copied to a ring in
 //            shared memory (cp.async.bulk).  Prefetching such rows in registers
 //            spilled, or left half of the threads: 1021 x 5003 fp32 backward took
@@ -22,7 +23,9 @@
 // writes one partial row, and a second small kernel adds the partial rows in a
 // fixed order: no atomics, the same bits every time.
 //
-// All sums are fp32: per thread over at most 16 elements of a row, then a tree.
+// All sums are fp32: per thread over at most 16 elements of a row (n / 512 of a wide
+// one), then a tree; down the rows, over the rows that a group (of wide ones: one
+// of 64 slices) takes in turn, then the join's tree.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
