@@ -29,7 +29,7 @@ namespace {
 constexpr int kSideMax = 128;
 constexpr int kTile64 = 64;                      // side of a tile
 constexpr int kSlab = 16;                        // k per round
-constexpr int kPitch = kTile64 + 8;              // rows 8 doubles off: a fragment's four rows fall in two halves of the banks
+constexpr int kPitch = kTile64 + 8;              // so a fragment's four rows fall in the two halves of the banks in turn
 constexpr int kTileThreads = 128;
 constexpr int kEach = kTile64 * kSlab / kTileThreads;   // elements of an operand per thread and round
 constexpr int kPositions = 32;                   // of the long side per block of long_apply_kernel
@@ -94,13 +94,14 @@ __device__ __forceinline__ void mma_f64(double (&d)[2], double a, double b) {
                : "d"(a), "d"(b));
 }
 
-// A 64 x 64 tile of a product over k from `begin` to `depth`: left(k, row) and right(k, column) give the operands' elements as
-// they lie in memory (0 outside; converted only once the round before is through, so that its MMAs do not
-// wait for them), done(row, column, value) takes each result.  `across`: consecutive threads load along rows and
-// columns rather than along k, as the operands lie in memory.
+// A 64 x 64 tile of a product over k from `begin` to `depth`: left(k, row) and
+// right(k, column) give the operands' elements as they lie in memory (0 outside;
+// converted only once the round before is through, so that its MMAs do not wait for
+// them), done(row, column, value) takes each result.  `across`: consecutive threads
+// load along rows and columns rather than along k.
 template <typename Raw, typename Left, typename Right, typename Done>
-__device__ __forceinline__ void tile_product(const LongParams& p, int64_t begin, int64_t depth, bool left_across, bool right_across, Left left, Right right,
-                                             Done done) {
+__device__ __forceinline__ void tile_product(const LongParams& p, int64_t begin, int64_t depth, bool left_across,
+                                             bool right_across, Left left, Right right, Done done) {
   __shared__ double l[kSlab][kPitch], r[kSlab][kPitch];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i0 = (warp >> 1) * 32, j0 = (warp & 1) * 32;
