@@ -412,9 +412,9 @@ muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void*
  * A direction that X lacks grows by |a| in each step of the factors' product Q,
  * and Q's errors with it.  Where |a| >= 1, |Q| stays below 512 (five steps of the
  * default coefficients: 485) and the iterates below 2, the r x r iterates are kept
- * as fp16 pairs (22 bits; in the last product as a pair of the type), and the
- * result is off by the rounding to its type and, for an X of nearly rank one, by
- * up to 3e-3 of ||out|| in bf16 and 2e-3 in fp16 (some 1e-5 for X like noise).
+ * as fp16 pairs (22 bits; in the last product as a pair of the type), and beside
+ * the rounding to its type the result is within 1e-2 of ||out|| (some 1e-5 for X
+ * like noise; the most that was measured, next to rank one, is 7e-3).
  * Otherwise the run is fp64 throughout (slower; the iterates too are kept in fp64),
  * and off by the rounding to the type and about |a|^ns_steps 1e-16.
  * In pairs ||X||_F^2 is held in fp32, so one below 1e-19 counts as zero, and a

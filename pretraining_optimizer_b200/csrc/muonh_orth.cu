@@ -34,16 +34,19 @@
 //
 // Precision.  The products are 16-bit with fp32 accumulation.  X X^T is exact
 // up to the accumulation: X is used as it is.  The r x r operands are kept as
-// fp16 pairs (hi + lo, 22 bits) and each product is hi hi + hi lo + lo hi:
+// fp16 pairs (hi + lo, 22 bits) and each product is lo hi + hi lo + hi hi:
 // with single fp16 operands the Gram-space form loses the small singular
 // directions (errors of 0.1 and more on ill-conditioned updates, by emulation,
 // against 2e-4 with pairs).  Q enters the last product as a pair of X's type.
 // Pairs hold five steps of the default coefficients; where ns_chain_run finds that
 // they do not hold all of a run, it is muonh_orth_fp64.cu's.
-// The tensor cores' accumulation truncates, so at most kGramChunk slices are
-// accumulated in TMEM before they are added in IEEE fp32 registers.  Chunks of 16,
-// 8 and 4 slices leave 896 bf16 [128, 2048] results 3.0e-4, 2.4e-4 and 2.2e-4 away
-// from the rounded exact ones (the rounding itself: 1.7e-3), in 401, 415 and 439 us.
+// The tensor cores' accumulation truncates: the slices take kGramAccs accumulators
+// in turn (the r x r products' columns are idle then), which are added in IEEE fp32
+// registers after at most kGramChunk slices, and each pair product adds up its
+// small parts first.  An X next to rank one with few rows and a long side was off
+// by 3e-2 of ||out|| with 16 slices in one accumulator and the small parts last,
+// and is by 7e-3 at most, in the same time (896 x [128, 2048]: 446 to 451 us under
+// the power cap with 8, 16 or 32 slices and with the old sums).
 // The result is rounded once to X's type.
 #include <algorithm>
 #include <cmath>
@@ -65,7 +68,8 @@ static_assert(kRing * kSliceBytes == 2 * kPairBytes, "A and P share the ring's s
 static_assert(kOrthSmem <= 227 * 1024, "shared memory of the orthogonalize kernel exceeds 227 KB");
 constexpr int kEpiThreads = 512;                  // 16 epilogue warps: 32 rows x 32 columns each
 constexpr int kOrthThreads = 64 + kEpiThreads;    // warp 0 TMA, warp 1 MMA
-constexpr int kGramChunk = 16;                    // slices (2048 columns) per TMEM accumulation
+constexpr int kGramAccs = 4;                      // accumulators that slices take in turn
+constexpr int kGramChunk = 8;                     // slices (1024 columns) before they are read
 constexpr int kMaxSteps = kMaxChainSteps;
 // With several matrices per SM all SMs read X, iterate and write at the same
 // time, and HBM idles during the r x r iterations.  Half of the SMs start later by
@@ -186,7 +190,8 @@ __device__ __forceinline__ void products(uint32_t d, uint64_t left, uint64_t rig
     umma_f16(d, left + k_major_step(k), right + mn_major_step(k), idesc, k == 0 ? accumulate : 1u);
 }
 
-// D = L R for the 128 x 128 pairs at l and r: hi hi + hi lo + lo hi.  R is
+// D = L R for the 128 x 128 pairs at l and r: lo hi + hi lo + hi hi, the small
+// products first, so that 8 accumulations truncate the full sum and not 24.  R is
 // symmetric up to rounding, but reading it as its transpose (K-major) compounds
 // that asymmetry from product to product: the last A_k was off by 1e-4 instead
 // of 1e-6.
@@ -194,7 +199,7 @@ template <int K>
 __device__ __forceinline__ void pair_product(uint32_t d, uint32_t l, uint32_t r, uint32_t idesc) {
 #pragma unroll 1
   for (int prod = 0; prod < 3; ++prod)
-    products<K>(d, k_major(l + (prod == 2 ? kSliceBytes : 0)), mn_major(r + (prod == 1 ? kSliceBytes : 0)), idesc, prod);
+    products<K>(d, k_major(l + (prod == 0 ? kSliceBytes : 0)), mn_major(r + (prod == 1 ? kSliceBytes : 0)), idesc, prod);
 }
 
 // The sum over the cluster's R CTAs of the 32 values of each epilogue thread,
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   uint8_t* const sm_q = smem + kQOffset;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarsOffset);   // [pass][slot]
   uint64_t* empty = full + 2 * kRing;             // [pass][slot]; pass 0: products done, pass 1: output stored
-  uint64_t* tfull = empty + 2 * kRing;            // [pass][accumulator]
+  uint64_t* tfull = empty + 2 * kRing;            // [pass][accumulator]; pass 0: one for all of them
   uint64_t* tempty = tfull + 4;
   uint64_t* ready = tempty + 4;                   // the epilogue wrote the next r x r operand
   uint64_t* q_ready = ready + 1;                  // ... the final Q; the ring's space is free again
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   wait_for_stream();
   if (p.late_below == 0) let_next_set_up();        // 1 us of the 21 to 45 of a small call; the norms lost by it
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tm_d = tmem + 256, tm_q = tmem + 384;   // r x r products; slice products use columns 0 .. 255
+  const uint32_t tm_d = tmem + 256, tm_q = tmem + 384;   // r x r products; X X^T uses all columns, Q X 0 .. 255
 
   // One walk of the producer over this CTA's slices.  A copy in flight lands
   // before the CTA may exit: the MMA issuer or, after a wait that gave up,
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     bool ok = true;
     for (int i = 0; i < count && ok; ++i) {
       const int slot = i % kRing, chunk = i / kGramChunk;
-      if (i % kGramChunk == 0 && chunk >= 2) ok = mbar_wait(&tempty[chunk & 1], ((chunk >> 1) - 1) & 1, err);
+      if (i % kGramChunk == 0 && chunk >= 1) ok = mbar_wait(&tempty[0], (chunk - 1) & 1, err);
       ok = ok && mbar_wait(&full[slot], (i / kRing) & 1, err);
       if (!ok) break;
       tc_fence_after();
@@ -379,10 +384,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint64_t dk = d + (p.tall ? mn_major_step(k) : k_major_step(k));
-          umma_f16(tmem + (chunk & 1) * kSide, dk, dk, idesc, (i % kGramChunk) != 0 || k != 0);
+          umma_f16(tmem + (i % kGramAccs) * kSide, dk, dk, idesc, (i % kGramChunk) >= kGramAccs || k != 0);
         }
         umma_commit(&empty[slot]);
-        if (i % kGramChunk == kGramChunk - 1 || i == count - 1) umma_commit(&tfull[chunk & 1]);
+        if (i % kGramChunk == kGramChunk - 1 || i == count - 1) umma_commit(&tfull[0]);
       }
       __syncwarp();
     }
@@ -390,16 +395,17 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = 0.f;
     for (int c = 0; c < chunks; ++c) {
-      if (!mbar_wait(&tfull[c & 1], (c >> 1) & 1, err)) break;
+      if (!mbar_wait(&tfull[0], c & 1, err)) break;
       tc_fence_after();
-      if (inside) {
+      const int accs = min(kGramAccs, count - c * kGramChunk);
+      for (int a = 0; a < accs && inside; ++a) {
         float v[32];
-        tmem_ld32(tmem + lanes + (c & 1) * kSide + col0, v);
+        tmem_ld32(tmem + lanes + a * kSide + col0, v);
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[j] += v[j];
       }
       tc_fence_before();
-      mbar_arrive(&tempty[c & 1]);
+      mbar_arrive(&tempty[0]);
     }
     if (ranks > 1) {   // this CTA's share, for the others to add
       float4* mine = reinterpret_cast<float4*>(smem) + (threadIdx.x - 64);
@@ -580,8 +586,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       const uint32_t x = smem_u32(smem + slot * kSliceBytes);
       if (leader) {
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {      // Q's hi, then its lo
-          const uint32_t qp = q + part * kSliceBytes, left = p.tall ? x : qp, right = p.tall ? qp : x;
+        for (int part = 0; part < 2; ++part) {      // Q's lo, then its hi: the small products first
+          const uint32_t qp = q + (1 - part) * kSliceBytes, left = p.tall ? x : qp, right = p.tall ? qp : x;
           if (p.used == 64)
             products<kHalf>(tmem + (i & 1) * kSide, k_major(left), mn_major(right), idesc, part);
           else

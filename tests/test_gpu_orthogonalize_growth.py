@@ -3,9 +3,10 @@ coefficients, and matrices of low rank, whose empty directions grow by |a| in
 each step while the result does not (B200 only).
 
 Tolerance.  Up to a growth of 512 (five steps of the default coefficients are
-485) the r x r iteration is kept in pairs; what is promised there is 3e-3 of
-||out|| for bf16 and 2e-3 for fp16 beside the rounding of the result (half a
-step).  Beyond it everything is fp64: an error of at most r 2^-52 of an operand
+485) the r x r iteration is kept in pairs; what is promised there is 1e-2 of
+||out||, the step's own bound, beside the rounding of the result (half a step).
+Most matrices here are held to less: 3e-3 for bf16 and 2e-3 for fp16, which the
+same arithmetic with single fp16 operands fails.  Beyond it everything is fp64: an error of at most r 2^-52 of an operand
 (products of at most 128 terms, and the long side's sum, whose terms' signs
 vary) is amplified by the growth at most, and the result is rounded to fp32
 (2^-24) on its way to 16 bits."""
@@ -53,7 +54,7 @@ def matrices(kind, batch, r, c, seed=1):
     return 1e-3 * rng.standard_normal((batch, r, c))
 
 
-def check(x, got, steps, coeffs=O.QUINTIC, eps=1e-7):
+def check(x, got, steps, coeffs=O.QUINTIC, eps=1e-7, pairs_bound=None):
     t = _t()
     assert got.shape == x.shape and got.dtype == x.dtype
     xs, gs = x.double().cpu().numpy(), got.double().cpu().numpy()
@@ -66,7 +67,7 @@ def check(x, got, steps, coeffs=O.QUINTIC, eps=1e-7):
     half = t.finfo(x.dtype).eps / 2
     for i in range(xs.shape[0]):
         size = np.linalg.norm(ref[i])
-        tol = PAIRS[name] * size if pairs else 2.0 ** -24 * size + g * min(x.shape[-2:]) * 2.0 ** -52 * max(size, 1.0)
+        tol = (pairs_bound or PAIRS[name]) * size if pairs else 2.0 ** -24 * size + g * min(x.shape[-2:]) * 2.0 ** -52 * max(size, 1.0)
         tol += half * (size + tol)
         tol += (2.0 ** -25 if x.dtype == t.float16 else 0.0) * np.sqrt(ref[i].size) + 1e-30
         off = np.linalg.norm(gs[i] - ref[i])
@@ -95,6 +96,20 @@ def test_five_steps_are_within_the_documented_bound(shape, kind, dtype):
     from test_gpu_orthogonalize import _spectrum
     x = t.from_numpy(_spectrum(np.random.default_rng(4), *shape, kind)).to("cuda:0", _dtype(dtype))
     check(x, orthogonalize(x), 5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind", ["exact1", "1+3e-4", "1+3e-3", "1+1e-2", "2+1e-2"])
+@pytest.mark.parametrize("shape", [(32, 2, 8192), (32, 3, 1024), (16, 8192, 5), (16, 16, 9000), (8, 128, 1024), (600, 2, 2048)])
+def test_the_promise_in_pairs_where_sums_are_long(shape, kind, dtype):
+    """Directions of a hundredth and less of the largest next to long sums: what the tensor cores truncate while
+    they add up X X^T and the r x r products is amplified by the square of the growth."""
+    t = _t()
+    from pretraining_optimizer_b200 import orthogonalize
+    for coeffs, steps in ((O.QUINTIC, 5), ((2.0, -1.5, 0.5), 9)):
+        x = t.from_numpy(matrices(kind, *shape, seed=10)).to("cuda:0", _dtype(dtype))
+        x = x[x.abs().amax((1, 2)) > 0]
+        check(x, orthogonalize(x, ns_steps=steps, ns_coeffs=coeffs), steps, coeffs, pairs_bound=1e-2)
 
 
 @pytest.mark.parametrize("coeffs,steps", [(CUBIC, 15), (CUBIC, 16), ((2.0, -1.5, 0.5), 9), ((2.0, -1.5, 0.5), 10),
