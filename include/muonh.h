@@ -479,8 +479,10 @@ typedef struct {
  *   d           row stride ldd elements of dtype (MUONH_DTYPE_*), overwritten;
  *               with accumulate != 0 (fp32 only) the product is added to it.
  *               Must not overlap the operands.
- * Products are accumulated in fp32 and rounded once to dtype.  k == 0 gives
- * zeros (or leaves an accumulated d as it is). */
+ * Products are accumulated in fp32 and rounded once to dtype.  The tensor cores
+ * truncate where they add (at most 2^-22 of the sum of |a b| per 32 of k): fp32
+ * results over 4096 of k, which are then added in IEEE fp32, 16-bit ones over all
+ * of it.  k == 0 gives zeros (or leaves an accumulated d as it is). */
 muonh_status muonh_block_matmul(const muonh_block_operand* a, const muonh_block_operand* b, int64_t k, void* d,
                                 int64_t ldd, int32_t dtype, int32_t accumulate, void* stream);
 

@@ -469,8 +469,8 @@ void ns_chain_scales(float a, float b, float c, int steps, int32_t* ea, int32_t*
 // By emulation of the kernel's arithmetic on nearly and exactly low-rank
 // matrices the result was off by up to 2.7e-3 of its norm (fp16: 1.6e-3) at a
 // growth of 485 (five steps of the default coefficients; 6.6e-3 with what the tensor
-// cores truncate), by 1e-2 at 1670, by 0.1 at 2e4, and overflowed at 2e5.  Factors below one (|a| < 1) would leave the pairs'
-// range at the other end.
+// cores truncate), by 1e-2 at 1670, by 0.1 at 2e4, and overflowed at 2e5.  Factors
+// below one (|a| < 1) would leave the pairs' range at the other end.
 constexpr double kPairGrowth = 512.0;    // bound on the product of the factors
 constexpr double kPairIterates = 2.0;    // ... and on the iterates' singular values (1.2 by default)
 int ns_chain_run(float a, float b, float c, int steps);
