@@ -417,9 +417,9 @@ muonh_status muonh_layer_norm_backward(const void* dy, int64_t lddy, const void*
  * like noise; the most that was measured, next to rank one, is 7e-3).
  * Otherwise the run is fp64 throughout (slower; the iterates too are kept in fp64),
  * and off by the rounding to the type and about |a|^ns_steps 1e-16.
- * In pairs ||X||_F^2 is held in fp32, so one below 1e-19 counts as zero, and a
- * matrix whose norm is above 1.8e19 gives NaN throughout, as one that holds NaN or
- * Inf does; the others are left alone.
+ * In pairs X X^T is held in fp32: without eps, norms below 1e-19 lose bits and
+ * below 1e-22 count as zero, and a matrix whose norm is above 1.8e19 gives NaN
+ * throughout, as one that holds NaN or Inf does; the others are left alone.
  *   workspace   16-byte aligned device scratch of muonh_orthogonalize_workspace
  *               bytes.  In pairs: 0 where base pointers and strides are multiples
  *               of 16 bytes, else room for a copy of the stacks that are not.  In
